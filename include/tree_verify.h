@@ -89,8 +89,11 @@ enum {
   TV_DEV_BAD_ROW = 8,       /* expansion row for a missing/expanded node,  */
                             /* or a malformed accepted path (commit)       */
   TV_DEV_BAD_LEN = 16,      /* n_nodes or prefix_len out of range          */
-  TV_DEV_TIMEOUT = 32       /* a bounded in-kernel wait expired; the       */
+  TV_DEV_TIMEOUT = 32,      /* a bounded in-kernel wait expired; the       */
                             /* affected outputs are NaN                    */
+  TV_DEV_BAD_PAGE = 64,     /* a page table entry in use outside           */
+                            /* [0, num_pages)                              */
+  TV_DEV_NO_PAGES = 128     /* the pool has fewer free pages than asked    */
 };
 
 typedef enum { TV_FP32 = 0, TV_BF16 = 1 } tv_dtype;
@@ -381,6 +384,249 @@ typedef struct {
 } tv_commit_args;
 
 TV_API tv_status tree_commit_kv(const tv_commit_args* a, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The cache in pages
+ *
+ * One verification step over a K/V cache kept in pages of page_size rows.
+ * The pool is k_pages, v_pages [num_pages][page_size][Hkv][d] (element
+ * strides kv_sp, kv_sr, kv_sh, shared by K and V; d contiguous); several
+ * layers lie kv_sl elements apart.  Row j of sequence b is row
+ * j % page_size of page page_table[b][j / page_size].  page_table is
+ * [B][max_pages] int32 with row stride pt_sb; entries that hold no row of a
+ * sequence are never looked at and may have any value (the calls below
+ * write -1).  A page may be shared by several sequences, and K/V rows past
+ * a sequence's end may hold anything, NaN included.
+ * ---------------------------------------------------------------------- */
+
+/* ------------------------------------------------------------------------
+ * tree_verify_attn_paged
+ *
+ * tree_verify_attn over a paged prefix: the same out and lse, with the
+ * prefix rows 0 .. prefix_len[b]-1 found through the page table and the
+ * tree K/V, parent[], n_nodes, scale, prefix_only and the faults as there
+ * (0 <= prefix_len[b] <= max_pages * page_size, else TV_DEV_BAD_LEN and NaN
+ * rows).  T = 1 is decoding of single tokens.  A sequence one of whose rows
+ * lies in a page outside [0, num_pages) gets NaN rows (TV_DEV_BAD_PAGE).
+ * K/V values of tree nodes that are not on a node's root path do not reach
+ * its rows, whatever they hold.
+ * dtype TV_FP32 or TV_BF16, d in {32, 64, 128}, Hq / Hkv <= 64,
+ * 1 <= page_size <= 65536; other values TV_ERR_UNSUPPORTED.  out may not
+ * overlap the inputs.  One launch; the split of the work over the GPU
+ * follows the lengths on the device, so max_pages costs nothing.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t dtype;
+  int32_t B, T, Hq, Hkv, d;
+  int32_t num_pages, page_size, max_pages;
+  const void* q;        int64_t q_sb, q_st, q_sh;
+  const void* k_pages;
+  const void* v_pages;  int64_t kv_sp, kv_sr, kv_sh;
+  const int32_t* page_table; int64_t pt_sb;
+  const int32_t* prefix_len;
+  const void* k_tree;
+  const void* v_tree;   int64_t kt_sb, kt_st, kt_sh;
+  const int32_t* parent; int64_t parent_sb;
+  const int32_t* n_nodes;
+  float scale;
+  void* out;            int64_t o_sb, o_st, o_sh;
+  float* lse;
+  uint32_t* dev_status;
+  int32_t prefix_only;
+} tv_attn_paged_args;
+
+TV_API size_t tree_verify_attn_paged_workspace_size(const tv_attn_paged_args* a);
+TV_API tv_status tree_verify_attn_paged(const tv_attn_paged_args* a, void* ws, size_t ws_bytes,
+                                        tv_stream_t stream);
+/* Which kernel tree_verify_attn_paged runs for these arguments: 0 = CUDA
+ * cores, 1 = tcgen05 (bf16, d in {64, 128}, page_size a multiple of 8,
+ * T <= 2048, 16-byte aligned bases and strides), -1 = rejected.  Host only. */
+TV_API int32_t tv_attn_paged_path(const tv_attn_paged_args* a);
+
+/* ------------------------------------------------------------------------
+ * tree_accept_probs
+ *
+ * The acceptance walk of tree_accept from given probabilities and given
+ * random numbers: for callers that shape the target's distribution
+ * themselves (top-p, penalties, a grammar's mask) and keep a random stream
+ * per request.  Row c of target_probs is p after node c, row c of
+ * draft_probs the distribution node c's children were drawn from.
+ *   SPECSAMPLE  child j (ascending index, token x_j) is accepted when
+ *               u_child[b][j] < p(x_j) / q_c(x_j) (q_c(x_j) = 0: when
+ *               p(x_j) > 0); on rejection p becomes (p - q_c)^+ /
+ *               sum (p - q_c)^+ (unchanged when that sum is 0); with every
+ *               child rejected (or at a leaf) the bonus token is the
+ *               smallest t with sum_{s<=t} p_s > u_sample[b][c] * sum p.
+ *   SPECEXEC    x = that sample of p at c; descend to the lowest-index child
+ *               carrying x, else emit x.
+ *   AUTO        SPECSAMPLE with draft_probs, else SPECEXEC.
+ * (GREEDY needs no random numbers: use tree_accept.)  p need not be
+ * normalised for the samples; the child test takes it as it is.  Sums are
+ * fp64.
+ *
+ * Inputs:  target_probs, draft_probs [B][T][V] fp32 (row strides tp_sb,
+ *          tp_st, dp_sb, dp_st; rows contiguous; draft_probs NULL for
+ *          SPECEXEC); draft_tokens, parent, n_nodes as in tree_accept;
+ *          u_child [B][T] fp64 (entry j: the test of node j; contiguous;
+ *          NULL for SPECEXEC), u_sample [B][T] fp64 (entry c: the sample at
+ *          node c; contiguous), in [0, 1).
+ * Outputs: n_accepted, accepted_nodes, out_tokens as in tree_accept.
+ * Only rows that the walk needs are read: a child test reads two numbers, a
+ * rejection or a sample the whole row.
+ * Faults as in tree_accept, except that values are checked where they are
+ * read: a negative or non-finite probability, a row to sample from that has
+ * no positive entry, or a uniform outside [0, 1) stops the walk with bonus
+ * -1 (TV_DEV_NONFINITE).
+ * 1 <= V <= 2^30, T <= 4096 (TV_ERR_UNSUPPORTED beyond).  No workspace.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t B, T, V;
+  const float* target_probs;   int64_t tp_sb, tp_st;
+  const float* draft_probs;    int64_t dp_sb, dp_st;
+  const int32_t* draft_tokens; int64_t tok_sb;
+  const int32_t* parent;       int64_t parent_sb;
+  const int32_t* n_nodes;
+  const double* u_child;
+  const double* u_sample;
+  int32_t mode;                /* tv_accept_mode, not GREEDY */
+  int32_t* n_accepted;
+  int32_t* accepted_nodes;
+  int32_t* out_tokens;
+  uint32_t* dev_status;
+} tv_accept_probs_args;
+
+TV_API tv_status tree_accept_probs(const tv_accept_probs_args* a, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * tree_commit_kv_paged
+ *
+ * tree_commit_kv into pages, for all layers in one launch: for layer l,
+ * sequence b with L = prefix_len[b], n = n_accepted[b] and the path rows
+ * (0, accepted_nodes[b][0 .. n-1]), row L + r of the sequence takes
+ * k_tree[l][b][rows[r]] (V likewise), then prefix_len_out[b] = L + n + 1.
+ * prefix_len_out may be prefix_len itself (advanced in place).
+ * Layouts: the pool as above with layer stride kv_sl; k_tree, v_tree
+ * [layers][B][T][Hkv][d] (kt_sl, kt_sb, kt_st, kt_sh).  The tree K/V may not
+ * overlap the pool, and no two sequences may commit into one page.
+ * dtype TV_FP32 or TV_BF16, 1 <= d <= 1024, B <= 16384.
+ * Faults: n outside [0, T-1], L negative or L + n + 1 > max_pages *
+ * page_size -> TV_DEV_BAD_LEN; a path node outside [1, T) or a path that
+ * does not increase -> TV_DEV_BAD_ROW; a page of the rows written outside
+ * [0, num_pages) -> TV_DEV_BAD_PAGE.  Such a sequence's pages are left as
+ * they were and its prefix_len_out is L.
+ * The workspace holds ticket counters (zeroed once, left zero by every
+ * call).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t dtype;
+  int32_t layers, B, T, Hkv, d;
+  int32_t num_pages, page_size, max_pages;
+  void* k_pages;
+  void* v_pages;        int64_t kv_sl, kv_sp, kv_sr, kv_sh;
+  const int32_t* page_table; int64_t pt_sb;
+  const int32_t* prefix_len;
+  int32_t* prefix_len_out;
+  const void* k_tree;
+  const void* v_tree;   int64_t kt_sl, kt_sb, kt_st, kt_sh;
+  const int32_t* n_accepted;
+  const int32_t* accepted_nodes; int64_t acc_sb;
+  uint32_t* dev_status;
+} tv_commit_paged_args;
+
+TV_API size_t tree_commit_kv_paged_workspace_size(const tv_commit_paged_args* a);
+TV_API tv_status tree_commit_kv_paged(const tv_commit_paged_args* a, void* ws, size_t ws_bytes,
+                                      tv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * tree_pages_update
+ *
+ * The next step's page tables from the present ones: sequences go on, fork,
+ * are rolled back, end, and get room to grow, in one call.  New sequence b
+ * keeps the first keep[b] rows of row source[b] of page_table (-1: a new,
+ * empty sequence; keep is then taken as 0) and gets room for grow[b] more
+ * rows that it alone will write.
+ *   - Pages of kept rows are shared, not copied, except a last page that is
+ *     only partly kept when grow[b] > 0 (b will write into it): b keeps the
+ *     page itself when no new sequence reads on in it, it is not pinned and
+ *     b is the first of those that will write into it; otherwise b gets a
+ *     fresh page and the kept rows of that page are copied (all layers).
+ *   - Fresh pages are the free pages, lowest index first, taken in the order
+ *     of (b, position).  Free is every page that no new sequence keeps and
+ *     that is not pinned: pages held by ended sequences or rolled-back rows
+ *     are free at once.  page_table must therefore hold every sequence of
+ *     the pool; pages held outside it (a prefix store) are listed as nonzero
+ *     in pinned.
+ *   - page_table_out[b] is -1 past the last page.  n_free is the number of
+ *     free pages left.
+ * With fewer free pages than needed nothing is copied, page_table_out is
+ * all -1, n_free is the (negative) difference and TV_DEV_NO_PAGES is set;
+ * page_table and its pages are as they were.
+ * Layouts: page_table [B_in][max_pages_in] (pt_sb), page_table_out
+ * [B][max_pages] (po_sb), which may not overlap page_table; source, keep,
+ * grow [B] int32; pinned [num_pages] int32 or NULL; n_free [1] or NULL.
+ * Limits: dtype TV_FP32 or TV_BF16, d <= 1024, B <= 16384, num_pages <=
+ * 2^24 (TV_ERR_UNSUPPORTED beyond).
+ * Faults: source outside [-1, B_in) -> TV_DEV_BAD_ROW; keep or grow
+ * negative, keep > max_pages_in * page_size or keep + grow > max_pages *
+ * page_size -> TV_DEV_BAD_LEN; a kept page outside [0, num_pages) ->
+ * TV_DEV_BAD_PAGE.  Such a sequence becomes empty (its row is -1).
+ * The workspace is zeroed once and left ready by every call.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t dtype;
+  int32_t layers, B_in, B, Hkv, d;
+  int32_t num_pages, page_size, max_pages_in, max_pages;
+  void* k_pages;
+  void* v_pages;        int64_t kv_sl, kv_sp, kv_sr, kv_sh;
+  const int32_t* page_table; int64_t pt_sb;
+  const int32_t* source;
+  const int32_t* keep;
+  const int32_t* grow;
+  const int32_t* pinned;
+  int32_t* page_table_out; int64_t po_sb;
+  int32_t* n_free;
+  uint32_t* dev_status;
+} tv_pages_update_args;
+
+TV_API size_t tree_pages_update_workspace_size(const tv_pages_update_args* a);
+TV_API tv_status tree_pages_update(const tv_pages_update_args* a, void* ws, size_t ws_bytes,
+                                   tv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * tree_pages_compact
+ *
+ * Moves the pages in use to the front of the pool.  Sequence b uses the
+ * first ceil(length[b] / page_size) entries of its page_table row; with
+ * n_used the number of pages used or pinned, the used pages at n_used or
+ * above that are not pinned move, in ascending order, to the free pages
+ * below n_used, in ascending order (whole pages, all layers), and
+ * page_table_out is page_table with the moved pages renamed and -1 past
+ * the used entries.  Every unpinned page in use is then below n_used.  Free
+ * pages keep what they held.
+ * page_table_out [B][max_pages] (po_sb) may be page_table itself (same
+ * stride); otherwise they may not overlap.  n_used [1] or NULL.  Other
+ * layouts and limits as in tree_pages_update.
+ * Faults: a length outside [0, max_pages * page_size] is clamped to that
+ * range (TV_DEV_BAD_LEN); a used entry outside [0, num_pages) is copied as
+ * it is (TV_DEV_BAD_PAGE).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t dtype;
+  int32_t layers, B, Hkv, d;
+  int32_t num_pages, page_size, max_pages;
+  void* k_pages;
+  void* v_pages;        int64_t kv_sl, kv_sp, kv_sr, kv_sh;
+  const int32_t* page_table; int64_t pt_sb;
+  const int32_t* length;
+  const int32_t* pinned;
+  int32_t* page_table_out; int64_t po_sb;
+  int32_t* n_used;
+  uint32_t* dev_status;
+} tv_pages_compact_args;
+
+TV_API size_t tree_pages_compact_workspace_size(const tv_pages_compact_args* a);
+TV_API tv_status tree_pages_compact(const tv_pages_compact_args* a, void* ws, size_t ws_bytes,
+                                    tv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Utilities

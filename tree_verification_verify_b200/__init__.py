@@ -10,6 +10,9 @@ CUDA device these functions raise.
                        deterministic-tree sampling)
     tree_expand_init / tree_expand_topb
                        batched best-first expansion rounds
+    tree_verify_attn_paged, tree_accept_probs, tree_commit_kv_paged,
+    tree_pages_update, tree_pages_compact
+                       verification over a paged cache (paged.py)
 """
 
 from __future__ import annotations
@@ -22,7 +25,8 @@ import torch
 
 __all__ = ["lib", "version", "status_string", "tree_verify_attn", "tree_verify_attn_merge", "tree_accept", "tree_accept_noalloc",
            "tree_expand_init", "tree_expand_topb", "ExpandState", "EXPAND_MODES", "tree_commit_kv", "philox_uniforms",
-           "TVError", "MODES"]
+           "tree_verify_attn_paged", "tree_accept_probs", "tree_commit_kv_paged", "tree_pages_update",
+           "tree_pages_compact", "TVError", "MODES"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtreeverify.so")
@@ -131,6 +135,7 @@ def lib() -> ctypes.CDLL:
         L.tree_verify_version.restype = ctypes.c_char_p
         L.tv_status_string.argtypes = [ctypes.c_int]
         L.tv_status_string.restype = ctypes.c_char_p
+        paged.bind(L)
         _lib = L
     return _lib
 
@@ -510,3 +515,10 @@ def expand_set_wait_limit(polls: int) -> None:
     tests per staged chunk in tree_expand_topb's row pass (0: default)."""
     _check(lib().tv_expand_set_wait_limit(int(polls)), "tv_expand_set_wait_limit")
 
+
+
+# --------------------------------------------------------------- paged cache
+
+from . import paged  # noqa: E402  (uses the checks above)
+from .paged import (tree_accept_probs, tree_commit_kv_paged, tree_pages_compact,  # noqa: E402
+                    tree_pages_update, tree_verify_attn_paged)

@@ -1,0 +1,719 @@
+// The paged cache's rows and pages: tree_commit_kv_paged, tree_pages_update,
+// tree_pages_compact.
+//
+// All three move rows of K and V between places that tables on the device
+// name.  Update and compaction run as two kernels.  The first, one cluster
+// of eight CTAs, marks the pages in use in a bitmap, ranks the free pages by
+// a prefix sum over its words and gives every sequence its place in that
+// list; its steps are separated by cluster barriers, so it needs neither a
+// cleared workspace nor a grid-wide wait.  The second writes the new tables
+// and copies the rows over the whole GPU.  Results depend on ranks alone,
+// never on the order in which threads arrive.
+#include <cooperative_groups.h>
+#include <initializer_list>
+
+#include "tv_common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace tv {
+
+namespace pages {
+
+constexpr int kThreads = 256;
+constexpr int kPlanThreads = 1024;               // of one CTA of the plan
+constexpr int kPlanCtas = 8;                     // a portable cluster
+constexpr int kTicketBytes = 64 * 1024;
+
+// Rows of one tensor: element strides of a (row, head) vector, and whether
+// the rows of a page follow one another without gaps.
+struct Pool {
+  char* k;
+  char* v;
+  int64_t sl, sp, sr, sh;      // bytes: layer, page, row, head
+  int Hkv, vec_bytes;          // bytes of a (row, head) vector
+  int dense;                   // a page's rows are one run of bytes
+};
+
+template <typename W>
+__device__ __forceinline__ W ldw(const char* p) { return *reinterpret_cast<const W*>(p); }
+template <typename W>
+__device__ __forceinline__ void stw(char* p, W v) { *reinterpret_cast<W*>(p) = v; }
+
+// Copies words [w0, w1) of `rows` rows from page address s to page address d
+// (byte offsets into k and v), by the calling CTA.
+template <typename W>
+__device__ __forceinline__ void copy_words(const Pool& pl, int64_t d, int64_t s, int w0, int w1) {
+  const int wpv = pl.vec_bytes / static_cast<int>(sizeof(W));
+  const int wpr = wpv * pl.Hkv;
+  constexpr int U = 4;
+  for (int i0 = w0 + threadIdx.x; i0 < w1; i0 += U * kThreads) {
+    W a[U], b[U];
+    int64_t off[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i < w1) {
+        if (pl.dense) {
+          off[u] = static_cast<int64_t>(i) * sizeof(W);
+        } else {
+          const int r = i / wpr, h = i % wpr / wpv, w = i % wpv;
+          off[u] = r * pl.sr + h * pl.sh + static_cast<int64_t>(w) * sizeof(W);
+        }
+        a[u] = ldw<W>(pl.k + s + off[u]);
+        b[u] = ldw<W>(pl.v + s + off[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * kThreads < w1) {
+        stw<W>(pl.k + d + off[u], a[u]);
+        stw<W>(pl.v + d + off[u], b[u]);
+      }
+    }
+  }
+}
+
+// Exclusive prefix sum of v over a CTA of the plan; *total is the sum.
+__device__ __forceinline__ int block_scan(int v, int* total) {
+  __shared__ int ws[kPlanThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  __syncthreads();                               // ws of the last call is read
+  if (lane == 31) ws[warp] = incl;
+  __syncthreads();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    before += w < warp ? ws[w] : 0;
+    sum += ws[w];
+  }
+  *total = sum;
+  return before + incl - v;
+}
+
+// The CTAs' shares of a sum: every CTA posts `mine`, and after a cluster
+// barrier the sum of the CTAs before this one and the whole sum are known.
+// `slots` is a place of kPlanCtas ints of its own for every call.
+__device__ __forceinline__ int cluster_base(cg::cluster_group& cl, int* slots, int mine, int* total) {
+  const int rank = static_cast<int>(cl.block_rank());
+  if (threadIdx.x < kPlanCtas) cl.map_shared_rank(slots, threadIdx.x)[rank] = mine;
+  cl.sync();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int c = 0; c < kPlanCtas; ++c) {
+    before += c < rank ? slots[c] : 0;
+    sum += slots[c];
+  }
+  *total = sum;
+  return before;
+}
+
+}  // namespace pages
+
+using namespace pages;
+
+// ------------------------------------------------------------------ commit
+
+struct CommitPagedParams {
+  Pool pool;
+  int layers, B, T, P, num_pages;
+  int64_t cap;                                   // rows of a table row
+  const int32_t* table; int64_t pt_sb;
+  const int32_t* len;
+  int32_t* len_out;
+  const char* kt; const char* vt; int64_t tl, tb, tt, th;   // bytes
+  const int32_t* n_acc;
+  const int32_t* acc; int64_t acc_sb;
+  int32_t* tickets;
+  uint32_t* status;
+};
+
+constexpr int kCommitRows = 256;                 // path rows looked up at a time
+
+// One CTA per (sequence, layer).  Path row r goes from tree node rows[r] to
+// row (L + r) % P of page table[(L + r) / P]; the rows' addresses are looked
+// up once per CTA into shared memory, then all (row, head) vectors are
+// copied word by word.  Every CTA checks the whole path and its pages before
+// it writes, so a sequence is committed in all layers or in none.
+template <typename W>
+__global__ void __launch_bounds__(kThreads) commit_paged_kernel(CommitPagedParams p) {
+  __shared__ int64_t s_src[kCommitRows], s_dst[kCommitRows];
+  const int b = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x;
+  const int L = p.len[b], n = p.n_acc[b];
+  const int32_t* acc = p.acc + b * p.acc_sb;
+  const int32_t* table = p.table + b * p.pt_sb;
+  const bool ok_len = n >= 0 && n < p.T && L >= 0 && static_cast<int64_t>(L) + n + 1 <= p.cap;
+  int bad = 0;
+  if (ok_len) {
+    for (int r = tid; r <= n; r += kThreads) {
+      const int x = r == 0 ? 0 : acc[r - 1];
+      if (r > 0 && (x < 1 || x >= p.T || (r > 1 && acc[r - 2] >= x))) bad |= 1;
+      const int page = table[(L + r) / p.P];
+      if (page < 0 || page >= p.num_pages) bad |= 2;
+      if (r < kCommitRows) {
+        s_src[r] = b * p.tb + x * p.tt;
+        s_dst[r] = page * p.pool.sp + static_cast<int64_t>((L + r) % p.P) * p.pool.sr;
+      }
+    }
+  }
+  const int bad_row = __syncthreads_or(bad & 1), bad_page = __syncthreads_or(bad & 2);
+  const bool ok = ok_len && !bad_row && !bad_page;
+  if (tid == 0 && layer == 0 && !ok)
+    set_status(p.status, !ok_len ? TV_DEV_BAD_LEN : (bad_row ? TV_DEV_BAD_ROW : 0u) | (bad_page ? TV_DEV_BAD_PAGE : 0u));
+  if (ok) {
+    const int wpv = p.pool.vec_bytes / static_cast<int>(sizeof(W));
+    const int wpr = wpv * p.pool.Hkv;
+    for (int r0 = 0; r0 <= n; r0 += kCommitRows) {
+      const int rows = min(kCommitRows, n + 1 - r0);
+      if (r0 > 0) {
+        __syncthreads();
+        if (tid < rows) {
+          const int r = r0 + tid;
+          s_src[tid] = b * p.tb + acc[r - 1] * p.tt;
+          s_dst[tid] = table[(L + r) / p.P] * p.pool.sp + static_cast<int64_t>((L + r) % p.P) * p.pool.sr;
+        }
+        __syncthreads();
+      }
+      for (int i = tid; i < rows * wpr; i += kThreads) {
+        const int r = i / wpr, h = i % wpr / wpv, w = i % wpv;
+        const int64_t s = layer * p.tl + s_src[r] + h * p.th + static_cast<int64_t>(w) * sizeof(W);
+        const int64_t d = layer * p.pool.sl + s_dst[r] + h * p.pool.sh + static_cast<int64_t>(w) * sizeof(W);
+        const W kw = ldw<W>(p.kt + s), vw = ldw<W>(p.vt + s);
+        stw<W>(p.pool.k + d, kw);
+        stw<W>(p.pool.v + d, vw);
+      }
+    }
+  }
+  // the sequence's last CTA to have read its length writes the new one
+  if (tid == 0) {
+    const int arrived = atomicAdd(p.tickets + b, 1);
+    if (arrived == p.layers - 1) {
+      p.tickets[b] = 0;
+      p.len_out[b] = ok ? L + n + 1 : L;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ update
+
+struct PlanHead {              // what the plan leaves for the second kernel
+  int32_t fail;                // update: fewer free pages than needed
+  int32_t moves;               // compact: pages that move
+  int32_t total;               // compact: pages used or pinned
+};
+
+struct UpdateParams {
+  Pool pool;
+  int layers, B_in, B, P, num_pages, W_in, W;
+  const int32_t* table; int64_t pt_sb;
+  const int32_t* source;
+  const int32_t* keep;
+  const int32_t* grow;
+  const int32_t* pinned;
+  int32_t* out; int64_t po_sb;
+  int32_t* n_free;
+  uint32_t* status;
+  // workspace
+  uint32_t* read;              // pages that some sequence, or a pin, reads on
+  uint32_t* write;             // partly kept last pages that a sequence goes on writing
+  int32_t* first;              // [page] the first such sequence (such pages only)
+  PlanHead* head;
+  int32_t* good;               // [B]
+  int32_t* off;                // [B] place of the sequence's fresh pages in the list; bit 31: copies its last page
+  int32_t* list;               // [num_pages] free pages, ascending, as many as are needed
+};
+
+struct Turn {
+  int s, keep, grow;
+  int held, want;              // pages kept, pages in all
+  bool partial;                // the last kept page is partly kept and will be written
+};
+
+__device__ __forceinline__ Turn turn_of(const UpdateParams& p, int b) {
+  Turn t;
+  t.s = p.source[b];
+  t.keep = t.s == -1 ? 0 : p.keep[b];
+  t.grow = p.grow[b];
+  t.held = t.want = 0;
+  t.partial = false;
+  return t;
+}
+__device__ __forceinline__ void turn_pages(const UpdateParams& p, Turn& t) {
+  t.held = static_cast<int>((static_cast<int64_t>(t.keep) + p.P - 1) / p.P);
+  t.want = static_cast<int>((static_cast<int64_t>(t.keep) + t.grow + p.P - 1) / p.P);
+  t.partial = t.keep % p.P != 0 && t.grow > 0;
+}
+
+// A warp's check of sequence b: the status bits of what is wrong with it.
+__device__ __forceinline__ uint32_t check_turn(const UpdateParams& p, Turn& t, const int32_t* row) {
+  uint32_t bits = 0;
+  if (t.s < -1 || t.s >= p.B_in) bits |= TV_DEV_BAD_ROW;
+  if (t.keep < 0 || t.grow < 0 || t.keep > static_cast<int64_t>(p.W_in) * p.P ||
+      static_cast<int64_t>(t.keep) + t.grow > static_cast<int64_t>(p.W) * p.P)
+    bits |= TV_DEV_BAD_LEN;
+  if (bits) return bits;
+  turn_pages(p, t);
+  bool bad = false;
+  for (int i = threadIdx.x & 31; i < t.held; i += 32) {
+    const int page = row[i];
+    bad |= page < 0 || page >= p.num_pages;
+  }
+  return __any_sync(0xffffffffu, bad) ? TV_DEV_BAD_PAGE : 0u;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) update_plan_kernel(UpdateParams p) {
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ int slots[3][kPlanCtas];
+  const int rank = static_cast<int>(cl.block_rank());
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int gtid = rank * kPlanThreads + tid, gsize = kPlanCtas * kPlanThreads;
+  const int gwarp = gtid >> 5, nwarp = gsize >> 5;
+  const int words = (p.num_pages + 31) / 32;
+  // 1: the pins, 32 pages to a warp's vote (or nothing), start the bitmap
+  for (int w = gwarp; w < words; w += nwarp) {
+    const int page = w * 32 + lane;
+    const bool pin = p.pinned && page < p.num_pages && p.pinned[page] != 0;
+    const unsigned m = __ballot_sync(0xffffffffu, pin);
+    if (lane == 0) {
+      p.read[w] = m;
+      p.write[w] = 0;
+    }
+  }
+  for (int b = gwarp; b < p.B; b += nwarp) {
+    Turn t = turn_of(p, b);
+    const int32_t* row = p.table + static_cast<int64_t>(max(t.s, 0)) * p.pt_sb;
+    const uint32_t bits = check_turn(p, t, row);
+    if (lane == 0) {
+      p.good[b] = bits == 0;
+      set_status(p.status, bits);
+      if (!bits && t.partial) p.first[row[t.held - 1]] = 0x7fffffff;
+    }
+  }
+  cl.sync();
+  // 2: the kept pages
+  for (int b = gwarp; b < p.B; b += nwarp) {
+    if (!__ldcg(p.good + b)) continue;
+    Turn t = turn_of(p, b);
+    turn_pages(p, t);
+    const int32_t* row = p.table + static_cast<int64_t>(max(t.s, 0)) * p.pt_sb;
+    for (int i = lane; i < t.held; i += 32) {
+      const int page = row[i];
+      if (t.partial && i == t.held - 1) {
+        atomicOr(p.write + (page >> 5), 1u << (page & 31));
+        atomicMin(p.first + page, b);
+      } else {
+        atomicOr(p.read + (page >> 5), 1u << (page & 31));
+      }
+    }
+  }
+  cl.sync();
+  // 3: every sequence's fresh pages and its place in the list.  CTA r takes
+  // sequences [r * per, ...), so the order is that of the sequences.
+  const int per = (p.B + kPlanCtas - 1) / kPlanCtas;
+  const int blo = min(p.B, rank * per), bhi = min(p.B, blo + per);
+  int need = 0;
+  for (int b0 = blo; b0 < bhi; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int mine = 0, copies = 0;
+    if (b < bhi && __ldcg(p.good + b)) {
+      Turn t = turn_of(p, b);
+      turn_pages(p, t);
+      mine = t.want - t.held;
+      if (t.partial) {
+        const int page = p.table[static_cast<int64_t>(t.s) * p.pt_sb + t.held - 1];
+        copies = ((__ldcg(p.read + (page >> 5)) >> (page & 31)) & 1u) || __ldcg(p.first + page) != b;
+        mine += copies;
+      }
+    }
+    int sum;
+    const int before = block_scan(mine, &sum);
+    if (b < bhi) p.off[b] = (need + before) | (copies ? 0x80000000 : 0);
+    need += sum;
+  }
+  int need_all, free_all;
+  const int need0 = cluster_base(cl, slots[0], need, &need_all);
+  for (int b = blo + tid; b < bhi; b += kPlanThreads) p.off[b] += need0;
+  // 4: the free pages in ascending order, words [r * pw, ...) in CTA r
+  const int pw = (words + kPlanCtas - 1) / kPlanCtas;
+  const int wlo = min(words, rank * pw), whi = min(words, wlo + pw);
+  auto free_word = [&](int w) -> uint32_t {
+    uint32_t f = ~(__ldcg(p.read + w) | __ldcg(p.write + w));
+    if (w == words - 1 && (p.num_pages & 31)) f &= (1u << (p.num_pages & 31)) - 1u;
+    return f;
+  };
+  int mine = 0, here;
+  for (int w = wlo + tid; w < whi; w += kPlanThreads) mine += __popc(free_word(w));
+  block_scan(mine, &here);
+  int at0 = cluster_base(cl, slots[1], here, &free_all);
+  for (int w0 = wlo; w0 < whi && at0 < need_all; w0 += kPlanThreads) {
+    const int w = w0 + tid;
+    uint32_t f = w < whi ? free_word(w) : 0u;
+    int sum;
+    int at = at0 + block_scan(__popc(f), &sum);
+    while (f && at < need_all) {
+      p.list[at++] = w * 32 + __ffs(f) - 1;
+      f &= f - 1u;
+    }
+    at0 += sum;
+  }
+  if (gtid == 0) {
+    p.head->fail = need_all > free_all;
+    if (need_all > free_all) set_status(p.status, TV_DEV_NO_PAGES);
+    if (p.n_free) *p.n_free = free_all - need_all;
+  }
+  cl.sync();                                     // no CTA's shared memory goes while a peer may post to it
+}
+
+// CTA (b, layer): the row of the new table (layer 0), and the kept rows of a
+// last page that b may not write into.
+template <typename W>
+__global__ void __launch_bounds__(kThreads) update_apply_kernel(UpdateParams p) {
+  const int b = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x;
+  const bool live = p.good[b] && !p.head->fail;
+  Turn t = turn_of(p, b);
+  if (live) turn_pages(p, t);
+  const int32_t* row = p.table + static_cast<int64_t>(max(t.s, 0)) * p.pt_sb;
+  const int at = p.off[b] & 0x7fffffff;
+  const bool copies = live && p.off[b] < 0;
+  if (layer == 0) {
+    const int fresh0 = t.held - (copies ? 1 : 0);      // first position of a fresh page
+    for (int i = tid; i < p.W; i += kThreads) {
+      int page = -1;
+      if (live && i < t.want) page = i < fresh0 ? row[i] : p.list[at + i - fresh0];
+      p.out[b * p.po_sb + i] = page;
+    }
+  }
+  if (copies && layer < p.layers) {
+    const int wpr = p.pool.Hkv * p.pool.vec_bytes / static_cast<int>(sizeof(W));
+    copy_words<W>(p.pool, layer * p.pool.sl + p.list[at] * p.pool.sp, layer * p.pool.sl + row[t.held - 1] * p.pool.sp,
+                  0, t.keep % p.P * wpr);
+  }
+}
+
+// ------------------------------------------------------------------ compact
+
+struct CompactParams {
+  Pool pool;
+  int layers, B, P, num_pages, W;
+  const int32_t* table; int64_t pt_sb;
+  const int32_t* length;
+  const int32_t* pinned;
+  int32_t* out; int64_t po_sb;
+  int32_t* n_used;
+  uint32_t* status;
+  // workspace
+  uint32_t* used;
+  uint32_t* pin;
+  PlanHead* head;
+  int32_t* from;               // [num_pages] pages that move, ascending
+  int32_t* to;                 // [num_pages] where they go (the holes, ascending)
+  int32_t* name;               // [num_pages] new index of a used page past the packed end
+};
+
+__device__ __forceinline__ int used_entries(const CompactParams& p, int len) {
+  const int64_t cap = static_cast<int64_t>(p.W) * p.P;
+  const int64_t n = len < 0 ? 0 : (len > cap ? cap : len);
+  return static_cast<int>((n + p.P - 1) / p.P);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CompactParams p) {
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ int slots[3][kPlanCtas];
+  const int rank = static_cast<int>(cl.block_rank());
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int gtid = rank * kPlanThreads + tid, gsize = kPlanCtas * kPlanThreads;
+  const int gwarp = gtid >> 5, nwarp = gsize >> 5;
+  const int words = (p.num_pages + 31) / 32;
+  for (int w = gwarp; w < words; w += nwarp) {
+    const int page = w * 32 + lane;
+    const unsigned m = __ballot_sync(0xffffffffu, p.pinned && page < p.num_pages && p.pinned[page] != 0);
+    if (lane == 0) {
+      p.used[w] = 0;
+      p.pin[w] = m;
+    }
+  }
+  cl.sync();
+  for (int b = gwarp; b < p.B; b += nwarp) {
+    const int len = p.length[b];
+    uint32_t bits = 0;
+    if (len < 0 || len > static_cast<int64_t>(p.W) * p.P) bits |= TV_DEV_BAD_LEN;
+    const int held = used_entries(p, len);
+    for (int i = lane; i < held; i += 32) {
+      const int page = p.table[b * p.pt_sb + i];
+      if (page < 0 || page >= p.num_pages) bits |= TV_DEV_BAD_PAGE;
+      else atomicOr(p.used + (page >> 5), 1u << (page & 31));
+    }
+    set_status(p.status, bits);
+  }
+  cl.sync();
+  // CTA r takes words [r * pw, ...): the pages that stay or move, then the
+  // holes below the packed end, then the pages above it
+  const int pw = (words + kPlanCtas - 1) / kPlanCtas;
+  const int wlo = min(words, rank * pw), whi = min(words, wlo + pw);
+  int mine = 0, here, total;
+  for (int w = wlo + tid; w < whi; w += kPlanThreads) mine += __popc(__ldcg(p.used + w) | __ldcg(p.pin + w));
+  block_scan(mine, &here);
+  cluster_base(cl, slots[0], here, &total);
+  auto below = [&](int w) -> uint32_t {            // bits of word w that lie below `total`
+    return w * 32 + 32 <= total ? 0xffffffffu : (w * 32 >= total ? 0u : (1u << (total - w * 32)) - 1u);
+  };
+  int holes = 0, moves = 0;
+  for (int w = wlo + tid; w < whi; w += kPlanThreads) {
+    const uint32_t u = __ldcg(p.used + w), pin = __ldcg(p.pin + w);
+    holes += __popc(~(u | pin) & below(w));
+    moves += __popc(u & ~pin & ~below(w));
+  }
+  int holes_here, moves_here, holes_all, moves_all;
+  block_scan(holes, &holes_here);
+  block_scan(moves, &moves_here);
+  int hat = cluster_base(cl, slots[1], holes_here, &holes_all);
+  int mat = cluster_base(cl, slots[2], moves_here, &moves_all);
+  for (int w0 = wlo; w0 < whi; w0 += kPlanThreads) {
+    const int w = w0 + tid;
+    uint32_t f = w < whi ? ~(__ldcg(p.used + w) | __ldcg(p.pin + w)) & below(w) : 0u;
+    int sum;
+    int at = hat + block_scan(__popc(f), &sum);
+    while (f) {
+      p.to[at++] = w * 32 + __ffs(f) - 1;
+      f &= f - 1u;
+    }
+    hat += sum;
+  }
+  cl.sync();                                       // the list of holes is whole
+  for (int w0 = wlo; w0 < whi; w0 += kPlanThreads) {
+    const int w = w0 + tid;
+    uint32_t u = 0, pin = 0;
+    if (w < whi) {
+      u = __ldcg(p.used + w) & ~below(w);
+      pin = __ldcg(p.pin + w);
+    }
+    int sum;
+    int at = mat + block_scan(__popc(u & ~pin), &sum);
+    while (u) {
+      const int bit = __ffs(u) - 1, page = w * 32 + bit;
+      if ((pin >> bit) & 1u) {
+        p.name[page] = page;
+      } else {
+        p.from[at] = page;
+        p.name[page] = __ldcg(p.to + at);
+        ++at;
+      }
+      u &= u - 1u;
+    }
+    mat += sum;
+  }
+  if (gtid == 0) {
+    p.head->moves = moves_all;
+    p.head->total = total;
+    if (p.n_used) *p.n_used = total;
+  }
+}
+
+// The tables' new names, then the pages, split over the grid in slices of
+// kSliceWords words of a page of one layer.
+constexpr int kSliceWords = 4 * kThreads;
+
+template <typename W>
+__global__ void __launch_bounds__(kThreads) compact_apply_kernel(CompactParams p) {
+  const int total = p.head->total, moves = p.head->moves;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const int held = used_entries(p, p.length[b]);
+    for (int i = threadIdx.x; i < p.W; i += kThreads) {
+      int page = -1;
+      if (i < held) {
+        page = p.table[b * p.pt_sb + i];
+        if (page >= total && page < p.num_pages) page = p.name[page];
+      }
+      p.out[b * p.po_sb + i] = page;
+    }
+  }
+  const int words = p.P * p.pool.Hkv * (p.pool.vec_bytes / static_cast<int>(sizeof(W)));
+  const int slices = (words + kSliceWords - 1) / kSliceWords;
+  const int64_t jobs = static_cast<int64_t>(moves) * p.layers * slices;
+  for (int64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
+    const int m = static_cast<int>(j / (p.layers * slices));
+    const int rest = static_cast<int>(j % (p.layers * slices));
+    const int layer = rest / slices, w0 = rest % slices * kSliceWords;
+    copy_words<W>(p.pool, layer * p.pool.sl + p.to[m] * p.pool.sp, layer * p.pool.sl + p.from[m] * p.pool.sp, w0,
+                  min(words, w0 + kSliceWords));
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+namespace {
+
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// Widest word that every base and every stride (bytes) and the vector allow.
+int word_bytes(std::initializer_list<const void*> bases, std::initializer_list<int64_t> strides) {
+  for (int w : {16, 4}) {
+    bool ok = true;
+    for (const void* b : bases) ok = ok && reinterpret_cast<uintptr_t>(b) % w == 0;
+    for (int64_t s : strides) ok = ok && s % w == 0;
+    if (ok) return w;
+  }
+  return 2;
+}
+
+template <typename A>
+Pool make_pool(const A* a) {
+  const int es = a->dtype == TV_BF16 ? 2 : 4;
+  Pool p;
+  p.k = static_cast<char*>(a->k_pages);
+  p.v = static_cast<char*>(a->v_pages);
+  p.sl = a->kv_sl * es; p.sp = a->kv_sp * es; p.sr = a->kv_sr * es; p.sh = a->kv_sh * es;
+  p.Hkv = a->Hkv;
+  p.vec_bytes = a->d * es;
+  p.dense = p.sh == p.vec_bytes && p.sr == static_cast<int64_t>(p.Hkv) * p.vec_bytes;
+  return p;
+}
+
+struct Carve {
+  unsigned char* base;
+  size_t off;
+  template <typename T>
+  T* take(size_t n) {
+    T* r = reinterpret_cast<T*>(base + off);
+    off = up256(off + n * sizeof(T));
+    return r;
+  }
+};
+
+}  // namespace
+
+namespace {
+
+size_t carve_update(unsigned char* ws, int B, int num_pages, UpdateParams& u) {
+  Carve c{ws, kTicketBytes};
+  const size_t words = (static_cast<size_t>(num_pages) + 31) / 32;
+  u.read = c.take<uint32_t>(words);
+  u.write = c.take<uint32_t>(words);
+  u.first = c.take<int32_t>(num_pages);
+  u.head = c.take<PlanHead>(1);
+  u.good = c.take<int32_t>(B);
+  u.off = c.take<int32_t>(B);
+  u.list = c.take<int32_t>(num_pages);
+  return c.off;
+}
+
+size_t carve_compact(unsigned char* ws, int num_pages, CompactParams& u) {
+  Carve c{ws, kTicketBytes};
+  const size_t words = (static_cast<size_t>(num_pages) + 31) / 32;
+  u.used = c.take<uint32_t>(words);
+  u.pin = c.take<uint32_t>(words);
+  u.head = c.take<PlanHead>(1);
+  u.from = c.take<int32_t>(num_pages);
+  u.to = c.take<int32_t>(num_pages);
+  u.name = c.take<int32_t>(num_pages);
+  return c.off;
+}
+
+template <typename P>
+cudaError_t launch_plan(void (*kernel)(P), const P& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kPlanCtas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kPlanCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+size_t commit_paged_workspace_bytes() { return kTicketBytes; }
+size_t pages_update_workspace_bytes(int B, int num_pages) {
+  UpdateParams u;
+  return carve_update(nullptr, B, num_pages, u);
+}
+size_t pages_compact_workspace_bytes(int num_pages) {
+  CompactParams u;
+  return carve_compact(nullptr, num_pages, u);
+}
+
+cudaError_t launch_commit_paged(const tv_commit_paged_args* a, void* ws, cudaStream_t stream) {
+  const int es = a->dtype == TV_BF16 ? 2 : 4;
+  CommitPagedParams p;
+  p.pool = make_pool(a);
+  p.layers = a->layers; p.B = a->B; p.T = a->T; p.P = a->page_size; p.num_pages = a->num_pages;
+  p.cap = static_cast<int64_t>(a->max_pages) * a->page_size;
+  p.table = a->page_table; p.pt_sb = a->pt_sb;
+  p.len = a->prefix_len;
+  p.len_out = a->prefix_len_out;
+  p.kt = static_cast<const char*>(a->k_tree);
+  p.vt = static_cast<const char*>(a->v_tree);
+  p.tl = a->kt_sl * es; p.tb = a->kt_sb * es; p.tt = a->kt_st * es; p.th = a->kt_sh * es;
+  p.n_acc = a->n_accepted;
+  p.acc = a->accepted_nodes; p.acc_sb = a->acc_sb;
+  p.tickets = static_cast<int32_t*>(ws);
+  p.status = a->dev_status;
+  const Pool& o = p.pool;
+  const dim3 grid(static_cast<unsigned>(a->B), static_cast<unsigned>(a->layers));
+  switch (word_bytes({o.k, o.v, p.kt, p.vt}, {o.sl, o.sp, o.sr, o.sh, o.vec_bytes, p.tl, p.tb, p.tt, p.th})) {
+    case 16: commit_paged_kernel<uint4><<<grid, kThreads, 0, stream>>>(p); break;
+    case 4: commit_paged_kernel<uint32_t><<<grid, kThreads, 0, stream>>>(p); break;
+    default: commit_paged_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_update(const tv_pages_update_args* a, void* ws, cudaStream_t stream) {
+  UpdateParams p;
+  p.pool = make_pool(a);
+  p.layers = a->layers; p.B_in = a->B_in; p.B = a->B; p.P = a->page_size; p.num_pages = a->num_pages;
+  p.W_in = a->max_pages_in; p.W = a->max_pages;
+  p.table = a->page_table; p.pt_sb = a->pt_sb;
+  p.source = a->source; p.keep = a->keep; p.grow = a->grow; p.pinned = a->pinned;
+  p.out = a->page_table_out; p.po_sb = a->po_sb;
+  p.n_free = a->n_free;
+  p.status = a->dev_status;
+  carve_update(static_cast<unsigned char*>(ws), a->B, a->num_pages, p);
+  cudaError_t e = launch_plan(update_plan_kernel, p, stream);
+  if (e != cudaSuccess || a->B == 0) return e;
+  const Pool& o = p.pool;
+  const dim3 grid(static_cast<unsigned>(a->B), static_cast<unsigned>(a->layers > 0 ? a->layers : 1));
+  switch (word_bytes({o.k, o.v}, {o.sl, o.sp, o.sr, o.sh, o.vec_bytes})) {
+    case 16: update_apply_kernel<uint4><<<grid, kThreads, 0, stream>>>(p); break;
+    case 4: update_apply_kernel<uint32_t><<<grid, kThreads, 0, stream>>>(p); break;
+    default: update_apply_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+int num_sms();
+
+cudaError_t launch_pages_compact(const tv_pages_compact_args* a, void* ws, cudaStream_t stream) {
+  CompactParams p;
+  p.pool = make_pool(a);
+  p.layers = a->layers; p.B = a->B; p.P = a->page_size; p.num_pages = a->num_pages; p.W = a->max_pages;
+  p.table = a->page_table; p.pt_sb = a->pt_sb;
+  p.length = a->length; p.pinned = a->pinned;
+  p.out = a->page_table_out; p.po_sb = a->po_sb;
+  p.n_used = a->n_used;
+  p.status = a->dev_status;
+  carve_compact(static_cast<unsigned char*>(ws), a->num_pages, p);
+  cudaError_t e = launch_plan(compact_plan_kernel, p, stream);
+  if (e != cudaSuccess) return e;
+  const Pool& o = p.pool;
+  const int grid = 8 * num_sms();
+  switch (word_bytes({o.k, o.v}, {o.sl, o.sp, o.sr, o.sh, o.vec_bytes})) {
+    case 16: compact_apply_kernel<uint4><<<grid, kThreads, 0, stream>>>(p); break;
+    case 4: compact_apply_kernel<uint32_t><<<grid, kThreads, 0, stream>>>(p); break;
+    default: compact_apply_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace tv
