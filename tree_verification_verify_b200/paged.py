@@ -124,7 +124,7 @@ def _vec(t, n, name, dtype=torch.int32):
 def _mat(t, rows, cols, name):
     """A [rows][cols] int32 table with contiguous rows."""
     if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != rows or (cols is not None and t.shape[1] != cols) or \
-            (t.shape[1] > 1 and t.stride(1) != 1):
+            (t.stride(1) != 1 and t.shape[1] > 1 and t.numel() > 0):
         raise _tv.TVError(f"{name} must be int32 [{rows}][{'...' if cols is None else cols}] with contiguous rows")
     return t
 
