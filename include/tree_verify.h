@@ -439,7 +439,7 @@ TV_API size_t tree_verify_attn_paged_workspace_size(const tv_attn_paged_args* a)
 TV_API tv_status tree_verify_attn_paged(const tv_attn_paged_args* a, void* ws, size_t ws_bytes,
                                         tv_stream_t stream);
 /* Which kernel tree_verify_attn_paged runs for these arguments: 0 = CUDA
- * cores, 1 = tcgen05 (bf16, d in {64, 128}, page_size a multiple of 8,
+ * cores, 1 = tcgen05 (bf16, d in {64, 128},
  * T <= 2048, 16-byte aligned bases and strides), -1 = rejected.  Host only. */
 TV_API int32_t tv_attn_paged_path(const tv_attn_paged_args* a);
 

@@ -1,6 +1,8 @@
 """GPU parity of tree_verify_attn_paged against the fp64 oracle, by an
 element-wise error bound (tests/paged_util.py)."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -240,6 +242,24 @@ def test_streams_and_graphs_have_scratch_of_their_own():
         e = tv.tree_verify_attn_paged(**args[0], stream=s[2])[0]
         torch.cuda.synchronize()
         assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and torch.equal(e, want[0])
+
+
+def test_the_shapes_the_tensor_cores_take():
+    import tree_verification_verify_b200 as tv
+    for kw, path in ((dict(d=128, P=16, dtype="bf16"), 1), (dict(d=64, P=5, dtype="bf16"), 1),
+                     (dict(d=128, P=16, dtype="fp32"), 0), (dict(d=32, P=16, dtype="bf16"), 0)):
+        c = AttnCase(1, 2, 4, 1, kw["d"], kw["P"], [20], kw["dtype"])
+        a = c.cuda()
+        p = tv.paged.AttnPagedArgs(dtype=int(kw["dtype"] == "bf16"), B=1, T=2, Hq=4, Hkv=1, d=kw["d"],
+                                   num_pages=a["k_pages"].shape[0], page_size=kw["P"], max_pages=2)
+        for f, x in (("q", "q"), ("k_pages", "k_pages"), ("v_pages", "v_pages"), ("page_table", "page_table"),
+                     ("prefix_len", "prefix_len"), ("k_tree", "k_tree"), ("v_tree", "v_tree"), ("parent", "parent"),
+                     ("out", "q")):
+            setattr(p, f, a[x].data_ptr())
+        d = kw["d"]
+        p.q_sb, p.q_st, p.q_sh, p.o_sb, p.o_st, p.o_sh = (8 * d, 4 * d, d) * 2
+        p.kv_sp, p.kv_sr, p.kv_sh, p.kt_sb, p.kt_st, p.kt_sh = kw["P"] * d, d, d, 2 * d, d, d
+        assert tv.lib().tv_attn_paged_path(ctypes.byref(p)) == path, kw
 
 
 def test_refusals():
