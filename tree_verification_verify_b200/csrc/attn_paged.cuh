@@ -10,9 +10,12 @@
 // and every CTA's stretch follow from prefix_len and n_nodes on the device,
 // so ragged batches are balanced to one tile, a long table costs nothing,
 // and a single long sequence fills the GPU.  A unit that crosses stretches
-// leaves one normalised partial and a log-sum-exp per piece in the workspace;
-// the last of its CTAs to finish (an atomic ticket) combines them, in piece
-// order, so results do not depend on the order of arrival.
+// leaves one normalised partial and a log-sum-exp per piece in the workspace,
+// and its first CTA a note of where they are; a second kernel, a warp per
+// row, combines them in piece order.  (The last CTA of a unit to finish did
+// that at first: 28 us for 128 rows of 9 pieces, where each of the warp's
+// dependent reads of another SM's fresh rows took about 1 us; spread over
+// the GPU it is a few us.)
 #pragma once
 
 #include "tv_common.cuh"
@@ -38,7 +41,13 @@ struct PagedAttnParams {
   int rows;                    // query rows of a row tile (tensor cores: node_tile * G)
   float* part_o;               // [CTA][2][tile rows][d]: the CTA's piece that continues a unit, that begins one
   float* part_lse;             // [CTA][2][tile rows], log2 units
-  int32_t* tickets;            // [CTA], zero between calls: arrivals at the unit split first in that CTA
+  struct SplitUnit* splits;    // [CTA] the unit that begins in that CTA and ends in a later one
+};
+
+// A unit in pieces: it begins in CTA c0 (the CTA's second slot) and goes on
+// in c0 + 1 .. c1 (their first); c1 < 0: none.
+struct SplitUnit {
+  int32_t c1, b, g, packed0, rows;
 };
 
 namespace paged {
@@ -73,12 +82,12 @@ constexpr int kMaxSlots = 512;
 
 // The line's prefix sums: slot t holds sequences [t * per, (t + 1) * per).
 struct Line {
-  int64_t cum[kMaxSlots + 1];
-  int64_t warp_sum[32];
+  int cum[kMaxSlots + 1];      // (the host refuses lines of 2^31 tiles)
+  int warp_sum[32];
   int per;                     // sequences per slot
   int nslot;
-  int64_t first, last;         // this CTA's stretch
-  int64_t step;                // tiles of a stretch
+  int first, last;             // this CTA's stretch
+  int step;                    // tiles of a stretch
 };
 
 // Called by all NT threads of the CTA (NT <= kMaxSlots, a multiple of 32).
@@ -86,30 +95,30 @@ template <int KEYS, int NT>
 __device__ __forceinline__ void build_line(const PagedAttnParams& p, Line& ln) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + NT - 1) / NT;
-  int64_t v = 0;
+  int v = 0;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b >= p.B) break;
     const SeqInfo s = seq_info<KEYS>(p, b);
-    v += static_cast<int64_t>(s.units) * s.len;
+    v += s.units * s.len;
     if (blockIdx.x == 0 && p.n_nodes) {
       const int n = p.n_nodes[b];
       if (n < 0 || n > p.T) set_status(p.status, TV_DEV_BAD_LEN);
     }
     if (blockIdx.x == 0 && s.bad_len && s.n > 0) set_status(p.status, TV_DEV_BAD_LEN);
   }
-  int64_t incl = v;
+  int incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+    const int t = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += t;
   }
   if (lane == 31) ln.warp_sum[warp] = incl;
   __syncthreads();
-  int64_t before = 0, total = 0;
+  int before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
-    const int64_t t = ln.warp_sum[w];
+    const int t = ln.warp_sum[w];
     before += w < warp ? t : 0;
     total += t;
   }
@@ -118,12 +127,14 @@ __device__ __forceinline__ void build_line(const PagedAttnParams& p, Line& ln) {
     ln.cum[NT] = total;
     ln.per = per;
     ln.nslot = NT;
-    const int64_t step = (total + gridDim.x - 1) / gridDim.x;
-    ln.step = step > 0 ? step : 1;
-    ln.first = min(total, ln.step * static_cast<int64_t>(blockIdx.x));
-    ln.last = min(total, ln.first + ln.step);
+    const int step = max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+    ln.step = step;
+    ln.first = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(step) * blockIdx.x));
+    ln.last = ln.first + min(step, total - ln.first);
   }
   __syncthreads();
+  // the merge kernel's CTAs may take the places of CTAs that end from here on
+  asm volatile("griddepcontrol.launch_dependents;");
 }
 
 // One piece: key tiles [t0, t1) of a unit.
@@ -131,32 +142,31 @@ struct Piece {
   int b, g, rt;
   SeqInfo s;
   int t0, t1;
-  int64_t unit_first;          // the unit's place in the line
+  int unit_first;              // the unit's place in the line
 };
 
 // The piece that begins at `pos` (ln.first <= pos < ln.last).
 template <int KEYS>
-__device__ __forceinline__ Piece piece_at(const PagedAttnParams& p, const Line& ln, int64_t pos) {
-  int lo = 0, hi = ln.nslot;                       // last slot whose sum is <= pos: the one that holds pos
+__device__ __forceinline__ Piece piece_at(const PagedAttnParams& p, const Line& ln, int pos) {
+  int lo = 0, hi = min(ln.nslot, p.B);             // last slot whose sum is <= pos: the one that holds pos
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (ln.cum[mid] <= pos) lo = mid; else hi = mid;
   }
   Piece c;
-  int64_t base = ln.cum[lo];
+  int base = ln.cum[lo];
   int b = lo * ln.per;
   for (int i = 0; i < ln.per; ++i, ++b) {          // one step when B is at most the thread count
     c.s = seq_info<KEYS>(p, b);
-    const int64_t w = static_cast<int64_t>(c.s.units) * c.s.len;
+    const int w = c.s.units * c.s.len;
     if (pos < base + w) break;
     base += w;
   }
   c.b = b;
-  const int64_t off = pos - base;
-  const int u = static_cast<int>(off / c.s.len);
-  c.t0 = static_cast<int>(off - static_cast<int64_t>(u) * c.s.len);
-  const int64_t left = ln.last - pos;
-  c.t1 = static_cast<int>(min(static_cast<int64_t>(c.s.len), c.t0 + left));
+  const int off = pos - base;
+  const int u = off / c.s.len;
+  c.t0 = off - u * c.s.len;
+  c.t1 = min(c.s.len, c.t0 + ln.last - pos);
   const int nrt = c.s.units / p.Hkv;
   c.g = u / nrt;
   c.rt = u - c.g * nrt;
@@ -168,72 +178,28 @@ __device__ __forceinline__ int64_t part_slot(const PagedAttnParams& p, int cta, 
   return (static_cast<int64_t>(cta) * 2 + which) * tile_rows;
 }
 
-// Where row r (node-major: node r / G, head r % G of kv head g) of a row
-// tile that starts at packed row r0 goes.
+// Where packed row r (node r / G, head r % G of kv head g) of sequence b goes.
 template <typename T>
-__device__ __forceinline__ T* out_row(const PagedAttnParams& p, const Piece& c, int packed) {
-  const int node = packed / p.G, head = c.g * p.G + packed % p.G;
-  return static_cast<T*>(p.out) + c.b * p.o_sb + static_cast<int64_t>(node) * p.o_st +
-         static_cast<int64_t>(head) * p.o_sh;
+__device__ __forceinline__ T* out_row(const PagedAttnParams& p, int b, int g, int packed) {
+  const int node = packed / p.G, head = g * p.G + packed % p.G;
+  return static_cast<T*>(p.out) + b * p.o_sb + static_cast<int64_t>(node) * p.o_st + static_cast<int64_t>(head) * p.o_sh;
 }
-__device__ __forceinline__ int64_t lse_row(const PagedAttnParams& p, const Piece& c, int packed) {
-  return (static_cast<int64_t>(c.b) * p.T + packed / p.G) * p.Hq + c.g * p.G + packed % p.G;
+__device__ __forceinline__ int64_t lse_row(const PagedAttnParams& p, int b, int g, int packed) {
+  return (static_cast<int64_t>(b) * p.T + packed / p.G) * p.Hq + g * p.G + packed % p.G;
+}
+
+// The note of a piece that begins a unit and does not end it.
+__device__ __forceinline__ SplitUnit split_of(const Line& ln, const Piece& c, int packed0, int rows) {
+  return SplitUnit{(c.unit_first + c.s.len - 1) / ln.step, c.b, c.g, packed0, rows};
 }
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Combines a split unit's partial rows and writes them out; called by a
-// whole warp per row.  c0 .. c1 are the CTAs that hold a piece: the unit
-// begins in c0 (its second slot) and goes on in the others (their first).
-//   M = max lse, w = 2^(lse - M), out = sum w o / sum w, lse = M + log2 sum w
-template <typename T, int D>
-__device__ __forceinline__ void merge_row(const PagedAttnParams& p, const Piece& c, int tile_rows, int r, int packed,
-                                          int c0, int c1) {
-  constexpr int DL = D / 32;
-  const int lane = threadIdx.x & 31;
-  float M = -INFINITY;
-  bool bad = false;
-  for (int k = c0 + lane; k <= c1; k += 32) {
-    const float v = __ldcg(p.part_lse + part_slot(p, k, k == c0 ? 1 : 0, tile_rows) + r);
-    bad |= v != v;
-    M = fmaxf(M, v);
-  }
-  bad = __any_sync(0xffffffffu, bad);
-  M = warp_max(M);
-  float acc[DL], den = 0.f;
-#pragma unroll
-  for (int e = 0; e < DL; ++e) acc[e] = 0.f;
-  if (!bad && M > -INFINITY) {
-#pragma unroll 8
-    for (int k = c0; k <= c1; ++k) {
-      const int64_t s = part_slot(p, k, k == c0 ? 1 : 0, tile_rows) + r;
-      const float v = __ldcg(p.part_lse + s);
-      const float w = exp2f(v - M);
-      float o[DL];
-      if (DL == 4) {
-        *reinterpret_cast<float4*>(o) = __ldcg(reinterpret_cast<const float4*>(p.part_o + s * D) + lane);
-      } else if (DL == 2) {
-        *reinterpret_cast<float2*>(o) = __ldcg(reinterpret_cast<const float2*>(p.part_o + s * D) + lane);
-      } else {
-        o[0] = __ldcg(p.part_o + s * D + lane);
-      }
-      den += w;
-      if (w != 0.f) {
-#pragma unroll
-        for (int e = 0; e < DL; ++e) acc[e] = fmaf(w, o[e], acc[e]);
-      }
-    }
-  }
-  const float inv = bad ? NAN : (den > 0.f ? 1.f / den : 0.f);
-  T* o = out_row<T>(p, c, packed) + lane * DL;
-#pragma unroll
-  for (int e = 0; e < DL; ++e) o[e] = static_cast<T>(bad ? NAN : acc[e] * inv);
-  if (lane == 0 && p.lse) p.lse[lse_row(p, c, packed)] = bad ? NAN : (M > -INFINITY ? (M + log2f(den)) * kLn2 : -INFINITY);
-}
-
 }  // namespace paged
 
 cudaError_t launch_attn_paged_simt(const PagedAttnParams& p, int grid, cudaStream_t stream);
+// Combines the split units' rows; tile_rows: rows of a partial's slot.
+cudaError_t launch_attn_paged_merge(const PagedAttnParams& p, int grid, int tile_rows, cudaStream_t stream);
 bool attn_paged_tc_supported(const tv_attn_paged_args* a);
 cudaError_t launch_attn_paged_tc(const PagedAttnParams& p, int grid, cudaStream_t stream);
 // Query rows of the CUDA-core kernel's row tile and its CTAs per SM.

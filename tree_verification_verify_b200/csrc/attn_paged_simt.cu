@@ -10,6 +10,8 @@
 //   S    a lane takes 64 / (32 WK) keys (or 32 WK / 64 lanes share one key's
 //        d); per 16 bytes of K it does 16 FMAs (4 rows);
 //   P V  a lane takes d / 32 columns; per V load it does 4 rows.
+#include <algorithm>
+
 #include "attn_paged.cuh"
 
 namespace tv {
@@ -65,7 +67,7 @@ attn_paged_simt_kernel(PagedAttnParams p, int vec) {
   __shared__ int64_t koff[2][kKeys];               // element offset of a key's row; -1: no key
   __shared__ uint64_t vis[R];                      // tree tile: keys that the row sees
   __shared__ int s_cur[R];                         // walk position on the row's root path
-  __shared__ int s_bad, s_badrow[R], s_last;
+  __shared__ int s_bad, s_badrow[R];
   float* qs = smem_f;                              // [R][D]
   float* ks = qs + R * D;                          // [64][D + 4]
   float* vs = ks + kKeys * KS;                     // [64][D]
@@ -74,8 +76,9 @@ attn_paged_simt_kernel(PagedAttnParams p, int vec) {
   const int wr = warp / WK, wk = warp % WK;
   const int G = p.G;
   build_line<kKeys, kThreads>(p, ln);
+  SplitUnit split = {-1, 0, 0, 0, 0};
 
-  for (int64_t pos = ln.first; pos < ln.last;) {
+  for (int pos = ln.first; pos < ln.last;) {
     const Piece c = piece_at<kKeys>(p, ln, pos);
     pos += c.t1 - c.t0;
     const int n = c.s.n, L = c.s.L;
@@ -285,10 +288,10 @@ attn_paged_simt_kernel(PagedAttnParams p, int vec) {
       const float inv = bad ? NAN : (empty ? 0.f : 1.f / den);
       const float lse = bad ? NAN : (empty ? -INFINITY : M + logf(den));
       if (whole) {
-        T* dst = out_row<T>(p, c, packed0 + row) + lane * DL;
+        T* dst = out_row<T>(p, c.b, c.g, packed0 + row) + lane * DL;
 #pragma unroll
         for (int e = 0; e < DL; ++e) dst[e] = static_cast<T>(empty && !bad ? 0.f : o[e] * inv);
-        if (lane == 0 && p.lse) p.lse[lse_row(p, c, packed0 + row)] = lse;
+        if (lane == 0 && p.lse) p.lse[lse_row(p, c.b, c.g, packed0 + row)] = lse;
       } else {
 #pragma unroll
         for (int e = 0; e < DL; ++e) p.part_o[(slot0 + row) * D + lane * DL + e] = empty && !bad ? 0.f : o[e] * inv;
@@ -297,23 +300,68 @@ attn_paged_simt_kernel(PagedAttnParams p, int vec) {
     }
     if (tid == 0 && s_bad) set_status(p.status, TV_DEV_BAD_PAGE);
     if (tid < rows && s_badrow[tid]) set_status(p.status, TV_DEV_BAD_PARENT);
-    if (!whole) {
-      const int c0 = static_cast<int>(c.unit_first / ln.step);
-      const int c1 = static_cast<int>((c.unit_first + c.s.len - 1) / ln.step);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int arrived = atomicAdd(p.tickets + c0, 1);
-        s_last = arrived == c1 - c0;
-        if (s_last) p.tickets[c0] = 0;             // the unit's last CTA leaves the counter ready
+    if (c.t0 == 0 && !whole) split = split_of(ln, c, packed0, rows);
+  }
+  if (tid == 0) p.splits[blockIdx.x] = split;
+}
+
+// A warp per row of a split unit:
+//   M = max lse, w = 2^(lse - M), out = sum w o / sum w, lse = M + log2 sum w
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) attn_paged_merge_kernel(PagedAttnParams p, int tile_rows) {
+  constexpr int DL = D / 32;
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kWarps + (threadIdx.x >> 5);
+#if defined(__CUDA_ARCH__)
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the first kernel's rows are there
+#endif
+  const SplitUnit u = p.splits[c0];
+  if (u.c1 < 0 || r >= u.rows) return;
+  // lane k: piece c0 + k's log-sum-exp (the first lies in the second slot of its CTA)
+  float M = -INFINITY;
+  bool bad = false;
+  for (int k = c0 + lane; k <= u.c1; k += 32) {
+    const float v = p.part_lse[part_slot(p, k, k == c0, tile_rows) + r];
+    bad |= v != v;
+    M = fmaxf(M, v);
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  M = warp_max(M);
+  float acc[DL], den = 0.f;
+#pragma unroll
+  for (int e = 0; e < DL; ++e) acc[e] = 0.f;
+  if (!bad && M > -INFINITY) {
+    constexpr int U = 8;                                   // pieces in flight
+    for (int k0 = c0; k0 <= u.c1; k0 += U) {
+      float o[U][DL], v[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int k = min(k0 + i, u.c1);
+        const int64_t s = part_slot(p, k, k == c0, tile_rows) + r;
+        v[i] = p.part_lse[s];
+        const float* src = p.part_o + s * D + lane * DL;
+        if (DL == 4) *reinterpret_cast<float4*>(o[i]) = *reinterpret_cast<const float4*>(src);
+        else if (DL == 2) *reinterpret_cast<float2*>(o[i]) = *reinterpret_cast<const float2*>(src);
+        else o[i][0] = src[0];
       }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        for (int r = warp; r < rows; r += kWarps) merge_row<T, D>(p, c, R, r, packed0 + r, c0, c1);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const float w = k0 + i <= u.c1 ? exp2f(v[i] - M) : 0.f;
+        den += w;
+        if (w != 0.f) {
+#pragma unroll
+          for (int e = 0; e < DL; ++e) acc[e] = fmaf(w, o[i][e], acc[e]);
+        }
       }
     }
   }
+  const float inv = bad ? NAN : (den > 0.f ? 1.f / den : 0.f);
+  const int packed = u.packed0 + r;
+  T* o = out_row<T>(p, u.b, u.g, packed) + lane * DL;
+#pragma unroll
+  for (int e = 0; e < DL; ++e) o[e] = static_cast<T>(bad ? NAN : acc[e] * inv);
+  if (lane == 0 && p.lse)
+    p.lse[lse_row(p, u.b, u.g, packed)] = bad ? NAN : (den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY);
 }
 
 namespace {
@@ -352,6 +400,40 @@ cudaError_t launch_d(const PagedAttnParams& p, int grid, int vec, cudaStream_t s
 // Rows of a tile: four to a warp, no more warps along the rows than a
 // sequence's rows fill.
 int attn_paged_simt_rows(int64_t rows) { return rows > 16 ? 32 : (rows > 8 ? 16 : (rows > 4 ? 8 : 4)); }
+
+namespace {
+
+template <typename T, int D>
+cudaError_t merge(const PagedAttnParams& p, int grid, int tile_rows, cudaStream_t stream) {
+  // The launch may overlap the first kernel's tail: every CTA waits for that kernel to end
+  const int most = static_cast<int>(std::min(static_cast<int64_t>(tile_rows), static_cast<int64_t>(p.T) * p.G));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, (most + kWarps - 1) / kWarps);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_paged_merge_kernel<T, D>, p, tile_rows);
+}
+
+template <typename T>
+cudaError_t merge_d(const PagedAttnParams& p, int grid, int tile_rows, cudaStream_t stream) {
+  switch (p.d) {
+    case 32: return merge<T, 32>(p, grid, tile_rows, stream);
+    case 64: return merge<T, 64>(p, grid, tile_rows, stream);
+    default: return merge<T, 128>(p, grid, tile_rows, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_paged_merge(const PagedAttnParams& p, int grid, int tile_rows, cudaStream_t stream) {
+  if (grid == 1) return cudaSuccess;                       // nothing is split
+  return p.dtype == TV_BF16 ? merge_d<__nv_bfloat16>(p, grid, tile_rows, stream) : merge_d<float>(p, grid, tile_rows, stream);
+}
 
 int attn_paged_simt_ctas(int, int d) { return d == 128 ? 2 : 4; }
 

@@ -10,12 +10,14 @@
 // unit while the softmax warps write the last one out.
 //
 // Warp roles (384 threads):
-//   warps 0-7  softmax and output: warps w and w + 4 own TMEM lanes
-//              32 (w % 4) .. (query rows), warp w < 4 keys 0-63 of a tile,
-//              warp w + 4 keys 64-127; the halves keep separate online
-//              softmax states and accumulators (O_0, O_1 in TMEM) that meet
-//              once per piece.  Warps without a valid row skip the
-//              arithmetic (decoding: G of 128 rows are real);
+//   warps 0-7  softmax and output: two warpgroups of a thread per query row
+//              (TMEM lane) take the tiles in turn, each with an online
+//              softmax state and an accumulator (O_0, O_1 in TMEM) of its
+//              own that meet once per piece.  One group's exponentials run
+//              while the other waits for TMEM and barriers (about 2000 of
+//              the 5000 cycles of a tile when both worked on halves of the
+//              same tile).  Warps without a valid row skip the arithmetic
+//              (decoding: G of 128 rows are real);
 //   warp 8     K tiles, warp 10 V tiles.  Page sizes that are multiples of
 //              8 rows: one TMA box per run of rows that both the page and
 //              the tile divide into (gcd(page size, 128) rows), a box per
@@ -23,11 +25,11 @@
 //              batch ahead.  Other page sizes: 16-byte cp.async per row
 //              into the same swizzled layout;
 //   warp 9     MMA: one thread polls what is ready and issues S = Q K^T two
-//              tiles ahead or O_h += P_h V_h (P read from TMEM), so neither
+//              tiles ahead or O_h += P V (P read from TMEM), so neither
 //              waits for the other's operands;
 //   warp 11    Q of the next unit, and parent[] for the tree tiles.
-// Online softmax in base 2; O is rescaled only when a row half's maximum
-// grows by more than 2^8 (P <= 256, exact in O / l).  P is rounded to bf16
+// Online softmax in base 2; O is rescaled only when a row's maximum grows by
+// more than 2^8 (P <= 256, exact in O / l).  P is rounded to bf16
 // for the product with V (the tensor cores' operand type); sums use the
 // unrounded fp32 weights.
 //
@@ -74,18 +76,45 @@ struct Shape {
 struct Bars {
   uint64_t q_full, q_empty;
   uint64_t k_full[6], k_empty[6], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_full[2][2], pv_done[2];           // [S buffer][column half]
+  uint64_t s_full[2], p_full[2], pv_done[2];              // by tile parity: S buffer, warpgroup, accumulator
+  uint64_t o_free;                                        // a piece's accumulators have been read
   uint64_t t_full[2], t_empty[2];                         // parent[] buffers
   uint32_t tmem_base;
   int abort;
   int bad_piece[8];                                       // piece number + 1 that met a bad page
-  uint32_t vbad[2][2][2];                                 // [tile parity][half] tree tile: V rows with infinities or NaN
-  int last;
+  uint32_t vbad[2][2][4];                                 // [group][its tile parity] V rows with infinities or NaN
   float red_m[2][kRows], red_l[2][kRows];
   uint8_t red_nf[2][kRows];
 };
 
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+// 16 consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  uint32_t u[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i]);
+  tmem_st16u(taddr, u);
+}
 
 // The real tiles of a piece: prefix tiles [a0, a1), tree tiles [b0, b1)
 // (tree tiles of later nodes than the row tile's are left out).
@@ -111,7 +140,7 @@ using namespace ptc;
 
 // Walks a CTA's pieces; every role has its own.
 struct PieceWalk {
-  int64_t pos;
+  int pos;
   int index;                    // pieces before this one
   int queue;                    // of those, pieces with tiles
   Piece c;
@@ -135,10 +164,9 @@ struct PieceWalk {
 
 // The MMA thread needs a piece's tile count alone.
 struct CountWalk {
-  int64_t pos;
-  int queue, cnt;
+  int pos, queue, cnt;
 };
-__device__ __noinline__ bool next_count(const PagedAttnParams& p, const Line& ln, CountWalk& x) {
+__device__ __forceinline__ bool next_count(const PagedAttnParams& p, const Line& ln, CountWalk& x) {
   PieceWalk w;
   w.pos = x.pos;
   w.index = 0;
@@ -164,6 +192,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   extern __shared__ uint8_t dsmem_raw[];
   __shared__ Bars bars;
   __shared__ Line ln;
+  __shared__ PieceWalk walks[kSoftmaxThreads / 32];       // the softmax warps': registers are for scores
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.G;
   const uint32_t raw = smem_u32(dsmem_raw);
@@ -172,17 +201,22 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   uint16_t* spar = reinterpret_cast<uint16_t*>(gbase + Sh::kPar);
   volatile int* abort = &bars.abort;
 
+  if (tid >= 32 && tid < 37) {
+    const CUtensorMap* m = tid == 32 ? &map_q : (tid == 33 ? &map_k : (tid == 34 ? &map_v : (tid == 35 ? &map_kt : &map_vt)));
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+  }
   if (tid == 0) {
     mbar_init(&bars.q_full, 1); mbar_init(&bars.q_empty, 1);
     for (int s = 0; s < KS; ++s) { mbar_init(&bars.k_full[s], 1); mbar_init(&bars.k_empty[s], 1); }
     for (int s = 0; s < VS; ++s) { mbar_init(&bars.v_full[s], 1); mbar_init(&bars.v_empty[s], 1); }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.s_full[s], 1);
-      mbar_init(&bars.p_full[s][0], 4); mbar_init(&bars.p_full[s][1], 4);
+      mbar_init(&bars.p_full[s], 4);
       mbar_init(&bars.pv_done[s], 1);
       mbar_init(&bars.t_full[s], 1); mbar_init(&bars.t_empty[s], 8);
-      for (int h = 0; h < 2; ++h) bars.vbad[s][h][0] = bars.vbad[s][h][1] = 0;
+      for (int i = 0; i < 8; ++i) bars.vbad[s][i >> 2][i & 3] = 0;
     }
+    mbar_init(&bars.o_free, 8);
     for (int i = 0; i < 8; ++i) bars.bad_piece[i] = 0;
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -201,6 +235,9 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   PieceWalk w;
   w.start(ln);
 
+  // 384 threads launch with 168 registers: 256 softmax threads take 208, the
+  // other 128 keep 88 (256 * 208 + 128 * 88 = 384 * 168)
+  if (warp >= kSoftmaxThreads / 32) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == kWarpK || warp == kWarpV) {
     // ------------------------------------------------------------ producers
     const bool isk = warp == kWarpK;
@@ -386,7 +423,6 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       CountWalk cs = {ln.first, -1, 0}, cp = cs;          // the pieces of the next S and of the next P V
       int rs = 0, rp = 0;                                 // tiles done in those pieces
       int is = 0, ip = 0;                                 // S and P V issued in all
-      int half = 0;                                       // halves issued of P V number ip
       bool more_s = next_count(p, ln, cs), more_p = more_s;
       cp = cs;
       auto step = [&](CountWalk& x, int& r, bool& more) {
@@ -402,10 +438,10 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         const bool tk = want_s && mbar_test(&bars.k_full[is % KS], (is / KS) & 1);
         const bool tq = want_s && (rs > 0 || mbar_test(&bars.q_full, cs.queue & 1));
         const bool want_p = ip < is;
-        const uint32_t pp = (ip >> 1) & 1;
-        const bool tv = want_p && (half > 0 || mbar_test(&bars.v_full[ip % VS], (ip / VS) & 1));
-        const bool t0 = want_p && (half > 0 || mbar_test(&bars.p_full[ip & 1][0], pp));
-        const bool t1 = want_p && mbar_test(&bars.p_full[ip & 1][1], pp);
+        const bool tv = want_p && mbar_test(&bars.v_full[ip % VS], (ip / VS) & 1);
+        const bool tp = want_p && mbar_test(&bars.p_full[ip & 1], (ip >> 1) & 1);
+        // the first tile of either group overwrites its accumulator, so the last piece's must have been read
+        const bool to = want_p && (rp > 1 || cp.queue == 0 || mbar_test(&bars.o_free, (cp.queue - 1) & 1));
         bool did = false;
         if (tk && tq) {
           fence_after();
@@ -424,27 +460,20 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           step(cs, rs, more_s);
           did = true;
         }
-        // O_h += P_h V_h: P_h is bf16 pairs over the first 32 columns of the
-        // half's S columns, V_h rows 64 h ..  The first tile of a piece
-        // overwrites both accumulators, so both halves must have read theirs.
-        if (tv && t0 && (half > 0 || rp > 0 || t1)) {
+        // O_h += P V: P is bf16 pairs over the first 64 columns of its S
+        if (tv && tp && to) {
           fence_after();
           const uint32_t sv = base + Sh::kV + (ip % VS) * TB;
-          for (; half < 2 && (half == 0 || t1); ++half) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ts(tmem + kColO + half * 128, tmem + kColS + (ip & 1) * 128 + 64 * half + kk * 8,
-                          smem_desc(sv + (4 * half + kk) * 2048, kHalfBytes, 1024), idesc_pv, (rp > 0 || kk > 0) ? 1u : 0u);
-            did = true;
-          }
-          if (half == 2) {
-            mma_commit(&bars.v_empty[ip % VS]);
-            mma_commit(&bars.pv_done[ip & 1]);
-            half = 0;
-            ++ip;
-            ++rp;
-            step(cp, rp, more_p);
-          }
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(tmem + kColO + (ip & 1) * 128, tmem + kColS + (ip & 1) * 128 + kk * 8,
+                        smem_desc(sv + kk * 2048, kHalfBytes, 1024), idesc_pv, (rp > 1 || kk > 0) ? 1u : 0u);
+          mma_commit(&bars.v_empty[ip % VS]);
+          mma_commit(&bars.pv_done[ip & 1]);
+          ++ip;
+          ++rp;
+          step(cp, rp, more_p);
+          did = true;
         }
         if (did) {
           idle = 0;
@@ -455,130 +484,179 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       }
       if (*abort) {
         // what was issued completes before the TMEM is freed
-        if (half > 0) mma_commit(&bars.pv_done[ip & 1]);
         for (int j = is > 2 ? is - 2 : 0; j < is; ++j) mbar_drain(&bars.s_full[j & 1], (j >> 1) & 1);
-        for (int j = ip > 1 ? ip - 1 : 0; j < ip + (half > 0); ++j) mbar_drain(&bars.pv_done[j & 1], (j >> 1) & 1);
+        for (int j = ip > 2 ? ip - 2 : 0; j < ip; ++j) mbar_drain(&bars.pv_done[j & 1], (j >> 1) & 1);
       }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax warps 0-7
-    const int row = tid & (kRows - 1), half = tid >> 7;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int row = tid & (kRows - 1), half = tid >> 7;   // half: the warpgroup
     const float sl2 = p.scale * 1.4426950408889634f;      // scores in log2 units
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t hcol = 64u * static_cast<uint32_t>(half);
-    const uint32_t ocol = kColO + 128u * static_cast<uint32_t>(half);
-    int it = 0, ntree = 0;
+    const uint32_t scol = trow + kColS + 128u * static_cast<uint32_t>(half);
+    const uint32_t ocol = trow + kColO + 128u * static_cast<uint32_t>(half);
+    int it0 = 0, ntree = 0;                               // tiles before this piece
+    SplitUnit split = {-1, 0, 0, 0, 0};
     bool ok = true;
-    while (w.next(p, ln)) {
+    PieceWalk& sw = walks[warp];
+    sw = w;
+    __syncwarp();
+    while (true) {
+      {
+        PieceWalk x = sw;
+        __syncwarp();
+        if (!x.next(p, ln)) break;
+        sw = x;
+        __syncwarp();
+      }
+      const PieceWalk& w = sw;
       const Piece& c = w.c;
       const int rows_here = w.nodes * G;
       const bool live = (warp & 3) * 32 < rows_here;      // the warp has valid rows
       const bool row_valid = row < rows_here;
       const int my_node = w.i0 + row / G;
-      const int na = w.t.a1 - w.t.a0;
+      const int na = w.t.a1 - w.t.a0, cnt = w.cnt, nodes = c.s.n;
+      const int keys0 = c.s.L - w.t.a0 * kKeys;           // prefix keys from the piece's first tile on
+      const int lo0 = (c.s.ntree - 1 - (w.t.b0 - na - c.s.nprefix)) * kKeys;
+      const int r0 = (half ^ it0) & 1;                    // the group's first tile
       float m_run = -INFINITY, l_run = 0.f;
       bool my_ok = true, nf = false;
-      int cur = -1;                                       // walk position on this row's root path
+      int cur = -2;                                       // walk position on this row's root path (-2: not begun)
       const uint16_t* par = spar + (ntree & 1) * kMaxT;
-      for (int r = 0; r < w.cnt; ++r, ++it) {
+      for (int r = r0; r < cnt; r += 2) {
+        const int it = it0 + r;
         const bool tree = r >= na;
-        const int lo = tree ? (c.s.ntree - 1 - (w.t.b0 + r - na - c.s.nprefix)) * kKeys : 0;
-        const int nk = tree ? min(kKeys, c.s.n - lo) : min(kKeys, c.s.L - (w.t.a0 + r) * kKeys);
+        const int lo = lo0 - r * kKeys;                   // tree tile: its first node
+        const int nk = min(kKeys, tree ? nodes - lo : keys0 - r * kKeys);
         const bool full = !tree && nk == kKeys;
-        if (r == na) {
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.t_full[ntree & 1], (ntree >> 1) & 1, abort));
-          cur = row_valid && ok ? my_node : -1;
-        }
-        // keys of this half that the row sees
-        uint32_t mkA = 0xffffffffu, mkB = 0xffffffffu;
+        // keys that the row sees
+        uint32_t mk[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         if (tree) {
-          mkA = mkB = 0u;
+          if (cur == -2) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.t_full[ntree & 1], (ntree >> 1) & 1, abort));
+            cur = row_valid && ok ? my_node : -1;
+          }
+          mk[0] = mk[1] = mk[2] = mk[3] = 0u;
           while (cur >= lo) {
             const int k = cur - lo;
-            if (k < kKeys && (k >> 6) == half) {
-              if (k & 32) mkB |= 1u << (k & 31); else mkA |= 1u << (k & 31);
-            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mk[i] |= (k >> 5) == i ? 1u << (k & 31) : 0u;
             const uint16_t up = par[cur];
             my_ok = my_ok && up != kBadMark;
             cur = up >= kRootMark ? -1 : static_cast<int>(up);
           }
         } else if (!full) {
-          const int nh = nk - 64 * half;
-          mkA = nh >= 32 ? 0xffffffffu : (nh <= 0 ? 0u : ((1u << nh) - 1u));
-          mkB = nh >= 64 ? 0xffffffffu : (nh <= 32 ? 0u : ((1u << (nh - 32)) - 1u));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int nh = nk - 32 * i;
+            mk[i] = nh >= 32 ? 0xffffffffu : (nh <= 0 ? 0u : ((1u << nh) - 1u));
+          }
         }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.s_full[it & 1], (it >> 1) & 1, abort));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.s_full[half], (it >> 1) & 1, abort));
         fence_after();
         if (live && ok) {
-          float s[64];
-          const uint32_t scol = kColS + (it & 1) * 128u;
-          tmem_ld32(trow + scol + hcol, s);
-          tmem_ld32(trow + scol + hcol + 32, s + 32);
-          tmem_wait_ld();
+          // Two forms of one computation: a full prefix tile holds its 128
+          // scores in registers; the others (one or two per piece) mask them,
+          // 32 at a time in loops that are not unrolled, and read them twice:
+          // code that runs once per piece is fetched each time, and fetching
+          // it costs more than running it.
+          float nmu, factor = 1.f;
+          bool grow;
+          auto take = [&](const float* mx) {              // the tile's maximum into the row's state
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+            const float m_new = fmaxf(m_run, mt);
+            grow = m_new > m_run + 8.0f;                  // also the first finite maximum
+            if (grow) {
+              factor = ex2_approx(m_run - m_new);         // 0 when m_run = -inf
+              m_run = m_new;
+            }
+            nmu = (m_run == -INFINITY) ? 0.f : -m_run;
+          };
+          // p = 2^(s sl2 - m) as bf16 pairs over the first half of S, behind
+          // the columns already read
+          float ps[4] = {0.f, 0.f, 0.f, 0.f};
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           if (full) {
+            float s[128];
 #pragma unroll
-            for (int k = 0; k < 64; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
-          } else {
+            for (int q = 0; q < 4; ++q) tmem_ld32(scol + q * 32, s + q * 32);
+            tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 64; ++k) {
-              const uint32_t mw = (k < 32) ? mkA : mkB;
-              s[k] = ((mw >> (k & 31)) & 1u) ? s[k] : -INFINITY;
-              mx[k & 3] = fmaxf(mx[k & 3], s[k]);
+            for (int k = 0; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
+            take(mx);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float a = ex2_approx(fmaf(s[q * 32 + k], sl2, nmu));
+                const float b = ex2_approx(fmaf(s[q * 32 + k + 1], sl2, nmu));
+                ps[k & 2] += a;
+                ps[(k & 2) + 1] += b;
+                pk[k / 2] = pack_bf16(a, b);
+              }
+              tmem_st16u(scol + q * 16, pk);
             }
-          }
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-          const float m_new = fmaxf(m_run, mt);
-          const bool grow = m_new > m_run + 8.0f;         // also the first finite maximum
-          float factor = 1.f;
-          if (grow) {
-            factor = ex2_approx(m_run - m_new);           // 0 when m_run = -inf
-            m_run = m_new;
-          }
-          const float nmu = (m_run == -INFINITY) ? 0.f : -m_run;
-          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+          } else {
+            auto mask = [&](int q) { return q == 0 ? mk[0] : (q == 1 ? mk[1] : (q == 2 ? mk[2] : mk[3])); };
+            float s[32];
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              tmem_ld32(scol + q * 32, s);
+              tmem_wait_ld();
+              const uint32_t m = mask(q);
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            s[k] = ex2_approx(fmaf(s[k], sl2, nmu));
-            ps[k & 3] += s[k];
+              for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], ((m >> k) & 1u) ? s[k] : -INFINITY);
+            }
+            take(mx);
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              tmem_ld32(scol + q * 32, s);
+              tmem_wait_ld();
+              const uint32_t m = mask(q);
+              uint32_t pk[16];
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float a = ((m >> k) & 1u) ? ex2_approx(fmaf(s[k], sl2, nmu)) : 0.f;
+                const float b = ((m >> (k + 1)) & 1u) ? ex2_approx(fmaf(s[k + 1], sl2, nmu)) : 0.f;
+                ps[k & 2] += a;
+                ps[(k & 2) + 1] += b;
+                pk[k / 2] = pack_bf16(a, b);
+              }
+              tmem_st16u(scol + q * 16, pk);
+              tmem_wait_st();
+            }
           }
           l_run = l_run * factor + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
-          if (__any_sync(0xffffffffu, grow) && r > 0) {
-            // O_h holds the tiles before this one: wait for the last P V, then rescale
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort));
+          if (__any_sync(0xffffffffu, grow) && r >= 2) {
+            // O_h holds the group's tiles before this one (their P V is done:
+            // this tile's S was issued behind it): rescale
             fence_after();
-            if (ok) {
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              float o[16];
+              tmem_ld16(ocol + q * 16, o);
+              tmem_wait_ld();
 #pragma unroll
-              for (int q = 0; q < D / 32; ++q) {
-                float o[32];
-                tmem_ld32(trow + ocol + q * 32, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= factor;
-                tmem_st32(trow + ocol + q * 32, o);
-              }
+              for (int e = 0; e < 16; ++e) o[e] *= factor;
+              tmem_st16(ocol + q * 16, o);
             }
           }
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(s[2 * e], s[2 * e + 1]);
-          tmem_st32u(trow + scol + hcol, pk);
           tmem_wait_st();
         }
-        if (tree || !full) {
+        if (!full) {
           // V rows that are no keys are cleared; a tree tile's rows are looked over
           ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.v_full[it % VS], (it / VS) & 1, abort));
-          const int vr = 64 * half + (row & 63), part = row >> 6;    // two threads of the half to a V row
-          constexpr int NC = D / 16;                                 // 16-byte chunks of a thread
-          uint8_t* v0 = gbase + Sh::kV + (it % VS) * TB + vr * 128;
+          uint8_t* v0 = gbase + Sh::kV + (it % VS) * TB + row * 128;
+          uint32_t* vbad = bars.vbad[half][(it >> 1) & 1];
           bool hit = false;
-          if (ok && (vr >= nk || tree)) {
-#pragma unroll
-            for (int q = 0; q < NC; ++q) {
-              const int ch = part * NC + q;
-              uint4* at = reinterpret_cast<uint4*>(v0 + (ch >> 3) * kHalfBytes + (((ch & 7) ^ (vr & 7)) << 4));
-              if (vr >= nk) {
+          if (ok && (row >= nk || tree)) {
+#pragma unroll 4
+            for (int ch = 0; ch < D / 8; ++ch) {
+              uint4* at = reinterpret_cast<uint4*>(v0 + (ch >> 3) * kHalfBytes + (((ch & 7) ^ (row & 7)) << 4));
+              if (row >= nk) {
                 *at = make_uint4(0u, 0u, 0u, 0u);
               } else {
                 uint4 x = *at;
@@ -593,64 +671,78 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
               }
             }
           }
-          if (hit) atomicOr(&bars.vbad[it & 1][half][(vr & 63) >> 5], 1u << (vr & 31));
+          if (hit) atomicOr(vbad + (row >> 5), 1u << (row & 31));
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           if (tree) {
-            // every warp of the half comes here for every tree tile, after an abort too
+            // every warp of the group comes here for every tree tile, after an abort too
             bar_sync(2 + half, 128);
-            const uint32_t b0 = *reinterpret_cast<volatile uint32_t*>(&bars.vbad[it & 1][half][0]);
-            const uint32_t b1 = *reinterpret_cast<volatile uint32_t*>(&bars.vbad[it & 1][half][1]);
-            if (b0 | b1) {
-              nf = nf || (mkA & b0) || (mkB & b1);
+            uint32_t any = 0, seen = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t x = *reinterpret_cast<volatile uint32_t*>(vbad + i);
+              any |= x;
+              seen |= x & mk[i];
+            }
+            if (any) {
+              nf = nf || seen;
               bar_sync(2 + half, 128);
-              if ((tid & 127) == 0) bars.vbad[it & 1][half][0] = bars.vbad[it & 1][half][1] = 0;
+              if ((tid & 127) < 4) vbad[tid & 3] = 0;
               bar_sync(2 + half, 128);
             }
           }
         }
         fence_before();
         __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(&bars.p_full[it & 1][half]);
+        if (lane == 0 && ok) mbar_arrive(&bars.p_full[half]);
       }
       // ---------------------------------------------------------- output
-      if (w.cnt > 0)
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort));
-      fence_after();
-      // the halves meet: M = max(m_0, m_1), c_h = 2^(m_h - M),
-      // O = (c_0 O_0 + c_1 O_1) / (c_0 l_0 + c_1 l_1); half h writes d columns DH h ..
+      // the group's last P V; tiles two apart complete in order, so one phase is enough
+      it0 += cnt;
+      if (cnt > r0) {
+        const int last = it0 - 1 - ((it0 - 1 - half) & 1);
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.pv_done[half], (last >> 1) & 1, abort));
+      }
+      // the groups meet: M = max(m_0, m_1), c_h = 2^(m_h - M),
+      // O = (c_0 O_0 + c_1 O_1) / (c_0 l_0 + c_1 l_1); group h writes d columns DH h ..
       bars.red_m[half][row] = m_run;
       bars.red_l[half][row] = l_run;
-      bars.red_nf[half][row] = nf;
+      bars.red_nf[half][row] = nf + 2 * !my_ok;
+      fence_before();
       bar_sync(1, kSoftmaxThreads);
+      fence_after();
       const float m_0 = bars.red_m[0][row], m_1 = bars.red_m[1][row];
       const float l_0 = bars.red_l[0][row], l_1 = bars.red_l[1][row];
-      nf = bars.red_nf[0][row] || bars.red_nf[1][row];
+      nf = ((bars.red_nf[0][row] | bars.red_nf[1][row]) & 1) != 0;
+      my_ok = ((bars.red_nf[0][row] | bars.red_nf[1][row]) & 2) == 0;
       const float M = fmaxf(m_0, m_1);
       const float c_0 = (m_0 == -INFINITY) ? 0.f : ex2_approx(m_0 - M);
       const float c_1 = (m_1 == -INFINITY) ? 0.f : ex2_approx(m_1 - M);
-      // a half whose sum is NaN (a NaN score) makes the row NaN
+      // a group whose sum is NaN (a NaN score) makes the row NaN
       const float l_row = c_0 * l_0 + c_1 * l_1 + ((l_0 != l_0 || l_1 != l_1) ? NAN : 0.f);
+      const bool have_0 = cnt > (it0 - cnt & 1 ? 1 : 0), have_1 = cnt > (it0 - cnt & 1 ? 0 : 1);   // tiles of group 0, 1
       const bool bad = c.s.bad_len || !my_ok || !ok || bars.bad_piece[w.index & 7] == w.index + 1;
       const bool empty = l_row == 0.f;
       const float inv = bad ? NAN : (empty ? 0.f : 1.f / l_row);
+      const float w_0 = c_0 * inv, w_1 = c_1 * inv;
       const bool whole = c.t0 == 0 && c.t1 == c.s.len;
       const int packed = w.i0 * G + row;
       const int which = c.t0 == 0 ? 1 : 0;
       const int64_t slot = part_slot(p, blockIdx.x, which, kRows) + row;
       if (live) {
-        __nv_bfloat16* orow = row_valid ? out_row<__nv_bfloat16>(p, c, packed) : nullptr;
-#pragma unroll
-        for (int q = 0; q < DH / 32; ++q) {
-          const int col = half * DH + q * 32;
-          float v0[32], v1[32];
-          if (w.cnt > 0) {                                // uniform over the warp
-            tmem_ld32(trow + kColO + col, v0);
-            tmem_ld32(trow + kColO + 128 + col, v1);
-            tmem_wait_ld();
-          }
+        __nv_bfloat16* orow = row_valid ? out_row<__nv_bfloat16>(p, c.b, c.g, packed) : nullptr;
+#pragma unroll 1
+        for (int q = 0; q < DH / 16; ++q) {
+          const int col = half * DH + q * 16;
+          float v0[16], v1[16];
+          if (have_0) tmem_ld16(trow + kColO + col, v0);
+          if (have_1) tmem_ld16(trow + kColO + 128 + col, v1);
+          tmem_wait_ld();
           if (!row_valid) continue;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v0[e] = bad ? NAN : (empty ? 0.f : fmaf(c_0, v0[e], c_1 * v1[e]) * inv);
+          for (int e = 0; e < 16; ++e) {
+            // an accumulator that no tile wrote is not looked at
+            v0[e] = (have_0 ? w_0 * v0[e] : 0.f) + (have_1 ? w_1 * v1[e] : 0.f) + (bad ? NAN : 0.f);
+          }
           if (nf) {
             // the values that are not finite, of the nodes this row sees
             int j = my_node;
@@ -658,7 +750,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
               const __nv_bfloat16* vs = static_cast<const __nv_bfloat16*>(p.vt) + c.b * p.kt_sb +
                                         static_cast<int64_t>(j) * p.kt_st + static_cast<int64_t>(c.g) * p.kt_sh + col;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
+              for (int e = 0; e < 16; ++e) {
                 const float x = __bfloat162float(vs[e]);
                 if (!(fabsf(x) < INFINITY)) v0[e] += x;
               }
@@ -669,7 +761,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           }
           if (whole) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
               uint4 x;
               x.x = pack_bf16(v0[8 * e], v0[8 * e + 1]);
               x.y = pack_bf16(v0[8 * e + 2], v0[8 * e + 3]);
@@ -679,7 +771,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 4; ++e)
               *reinterpret_cast<float4*>(p.part_o + slot * D + col + 4 * e) =
                   make_float4(v0[4 * e], v0[4 * e + 1], v0[4 * e + 2], v0[4 * e + 3]);
           }
@@ -687,10 +779,14 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (half == 0 && row_valid) {
           const float lse2 = bad ? NAN : (empty ? -INFINITY : M + log2f(l_row));
           if (!whole) p.part_lse[slot] = lse2;
-          else if (p.lse) p.lse[lse_row(p, c, packed)] = lse2 * kLn2;
+          else if (p.lse) p.lse[lse_row(p, c.b, c.g, packed)] = lse2 * kLn2;
           if (!my_ok) set_status(p.status, TV_DEV_BAD_PARENT);
         }
       }
+      // the accumulators are free for the next piece
+      fence_before();
+      __syncwarp();
+      if (lane == 0 && cnt > 0) mbar_arrive(&bars.o_free);
       if (tid == 0) {
         if (bars.bad_piece[w.index & 7] == w.index + 1) set_status(p.status, TV_DEV_BAD_PAGE);
         if (!ok) set_status(p.status, TV_DEV_TIMEOUT);
@@ -700,26 +796,10 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (lane == 0) mbar_arrive(&bars.t_empty[ntree & 1]);
         ++ntree;
       }
-      fence_before();
-      if (!whole) {
-        const int c0 = static_cast<int>(c.unit_first / ln.step);
-        const int c1 = static_cast<int>((c.unit_first + c.s.len - 1) / ln.step);
-        __threadfence();
-        bar_sync(1, kSoftmaxThreads);
-        if (tid == 0) {
-          const int arrived = atomicAdd(p.tickets + c0, 1);
-          bars.last = arrived == c1 - c0;
-          if (arrived == c1 - c0) p.tickets[c0] = 0;      // the unit's last CTA leaves the counter ready
-        }
-        bar_sync(1, kSoftmaxThreads);
-        if (*reinterpret_cast<volatile int*>(&bars.last)) {
-          __threadfence();
-          for (int r = warp; r < rows_here; r += kSoftmaxThreads / 32)
-            merge_row<__nv_bfloat16, D>(p, c, kRows, r, w.i0 * G + r, c0, c1);
-        }
-      }
-      bar_sync(1, kSoftmaxThreads);                       // red_*, last: read by all
+      if (tid == 0 && c.t0 == 0 && !whole) split = split_of(ln, c, w.i0 * G, rows_here);
+      bar_sync(1, kSoftmaxThreads);                       // red_*: read by all
     }
+    if (tid == 0) p.splits[blockIdx.x] = split;
   }
   fence_before();
   __syncthreads();

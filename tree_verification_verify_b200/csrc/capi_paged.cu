@@ -75,7 +75,8 @@ tv_status check_attn_paged(const tv_attn_paged_args* a) {
 struct PagedPlan {
   bool tc;
   int rows, grid;
-  size_t off_o, off_lse, total;
+  bool fits;                   // the line has fewer than 2^31 key tiles
+  size_t off_o, off_lse, off_splits, total;
 };
 
 PagedPlan plan_attn_paged(const tv_attn_paged_args* a) {
@@ -88,6 +89,7 @@ PagedPlan plan_attn_paged(const tv_attn_paged_args* a) {
   const int64_t rt = (static_cast<int64_t>(a->T) * G + pl.rows - 1) / pl.rows;
   const int64_t tiles = (static_cast<int64_t>(a->max_pages) * a->page_size + keys - 1) / keys + (a->T + keys - 1) / keys;
   const int64_t most = static_cast<int64_t>(a->B) * a->Hkv * rt * (tiles > 0 ? tiles : 1);
+  pl.fits = most < (1ll << 31);
   const int64_t want = static_cast<int64_t>(num_sms()) * (pl.tc ? 1 : attn_paged_simt_ctas(pl.rows, a->d));
   pl.grid = static_cast<int>(most < want ? (most > 0 ? most : 1) : want);
   const size_t tile_rows = pl.tc ? 128 : pl.rows;
@@ -95,6 +97,7 @@ PagedPlan plan_attn_paged(const tv_attn_paged_args* a) {
   size_t off = kTicketBytes;
   pl.off_o = off;   off = align256(off + slots * a->d * sizeof(float));
   pl.off_lse = off; off = align256(off + slots * sizeof(float));
+  pl.off_splits = off; off = align256(off + pl.grid * sizeof(SplitUnit));
   pl.total = off;
   return pl;
 }
@@ -103,12 +106,14 @@ PagedPlan plan_attn_paged(const tv_attn_paged_args* a) {
 
 extern "C" size_t tree_verify_attn_paged_workspace_size(const tv_attn_paged_args* a) {
   if (check_attn_paged(a) != TV_OK) return 0;
-  return plan_attn_paged(a).total;
+  const PagedPlan pl = plan_attn_paged(a);
+  return pl.fits ? pl.total : 0;
 }
 
 extern "C" int32_t tv_attn_paged_path(const tv_attn_paged_args* a) {
   if (check_attn_paged(a) != TV_OK) return -1;
-  return plan_attn_paged(a).tc ? 1 : 0;
+  const PagedPlan pl = plan_attn_paged(a);
+  return pl.fits ? (pl.tc ? 1 : 0) : -1;
 }
 
 extern "C" tv_status tree_verify_attn_paged(const tv_attn_paged_args* a, void* ws, size_t ws_bytes,
@@ -117,6 +122,7 @@ extern "C" tv_status tree_verify_attn_paged(const tv_attn_paged_args* a, void* w
   if (st != TV_OK) return st;
   if (a->B == 0 || a->T == 0) return TV_OK;
   const PagedPlan pl = plan_attn_paged(a);
+  if (!pl.fits) return TV_ERR_UNSUPPORTED;
   if (!ws_ok(ws, ws_bytes, pl.total)) return TV_ERR_WORKSPACE;
   PagedAttnParams p;
   std::memset(&p, 0, sizeof(p));
@@ -137,11 +143,13 @@ extern "C" tv_status tree_verify_attn_paged(const tv_attn_paged_args* a, void* w
   p.prefix_only = a->prefix_only;
   p.rows = pl.rows;
   unsigned char* w = static_cast<unsigned char*>(ws);
-  p.tickets = reinterpret_cast<int32_t*>(w);
+  p.splits = reinterpret_cast<SplitUnit*>(w + pl.off_splits);
   p.part_o = reinterpret_cast<float*>(w + pl.off_o);
   p.part_lse = reinterpret_cast<float*>(w + pl.off_lse);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return from_cuda(pl.tc ? launch_attn_paged_tc(p, pl.grid, s) : launch_attn_paged_simt(p, pl.grid, s));
+  const cudaError_t e = pl.tc ? launch_attn_paged_tc(p, pl.grid, s) : launch_attn_paged_simt(p, pl.grid, s);
+  if (e != cudaSuccess) return TV_ERR_CUDA;
+  return from_cuda(launch_attn_paged_merge(p, pl.grid, pl.tc ? 128 : pl.rows, s));
 }
 
 // ------------------------------------------------------------ acceptance
