@@ -38,9 +38,10 @@ struct PagedAttnParams {
   float* lse;
   uint32_t* status;
   int prefix_only;
-  int rows;                    // query rows of a row tile (tensor cores: node_tile * G)
-  float* part_o;               // [CTA][2][tile rows][d]: the CTA's piece that continues a unit, that begins one
-  float* part_lse;             // [CTA][2][tile rows], log2 units
+  int rows;                    // query rows of a unit
+  int box;                     // tensor cores: rows of a page that one TMA box takes (0: row by row)
+  float* part_o;               // [CTA][2][rows][d]: the CTA's piece that continues a unit, that begins one
+  float* part_lse;             // [CTA][2][rows], log2 units
   struct SplitUnit* splits;    // [CTA] the unit that begins in that CTA and ends in a later one
 };
 
@@ -58,12 +59,15 @@ struct SeqInfo {
   int L;                       // prefix rows (0 when prefix_len is out of range)
   bool bad_len;
   int nprefix, ntree;          // key tiles of a unit
+  int rem, off;                // the prefix's last rem rows share the one tree tile, whose nodes begin at row off
   int len;                     // max(1, nprefix + ntree): a unit without keys still writes its rows
   int units;                   // row tiles * kv heads
 };
 
+// align > 0: the prefix's rows past its whole tiles and a tree of at most one
+// tile go into one tile where they fit (nodes at a multiple of align).
 template <int KEYS>
-__device__ __forceinline__ SeqInfo seq_info(const PagedAttnParams& p, int b) {
+__device__ __forceinline__ SeqInfo seq_info(const PagedAttnParams& p, int b, int align) {
   SeqInfo s;
   const int n = p.n_nodes ? p.n_nodes[b] : p.T;
   const int L = p.prefix_len[b];
@@ -73,6 +77,13 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedAttnParams& p, int b) {
   s.L = s.bad_len ? 0 : L;
   s.nprefix = (s.L + KEYS - 1) / KEYS;
   s.ntree = p.prefix_only ? 0 : (s.n + KEYS - 1) / KEYS;
+  s.rem = s.off = 0;
+  const int rem = s.L % KEYS, off = align > 0 ? (rem + align - 1) / align * align : 0;
+  if (align > 0 && s.ntree == 1 && rem > 0 && off + s.n <= KEYS) {
+    --s.nprefix;
+    s.rem = rem;
+    s.off = off;
+  }
   s.len = max(1, s.nprefix + s.ntree);
   s.units = (s.n * p.G + p.rows - 1) / p.rows * p.Hkv;
   return s;
@@ -92,14 +103,14 @@ struct Line {
 
 // Called by all NT threads of the CTA (NT <= kMaxSlots, a multiple of 32).
 template <int KEYS, int NT>
-__device__ __forceinline__ void build_line(const PagedAttnParams& p, Line& ln) {
+__device__ __forceinline__ void build_line(const PagedAttnParams& p, Line& ln, int align) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + NT - 1) / NT;
   int v = 0;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b >= p.B) break;
-    const SeqInfo s = seq_info<KEYS>(p, b);
+    const SeqInfo s = seq_info<KEYS>(p, b, align);
     v += s.units * s.len;
     if (blockIdx.x == 0 && p.n_nodes) {
       const int n = p.n_nodes[b];
@@ -147,7 +158,7 @@ struct Piece {
 
 // The piece that begins at `pos` (ln.first <= pos < ln.last).
 template <int KEYS>
-__device__ __forceinline__ Piece piece_at(const PagedAttnParams& p, const Line& ln, int pos) {
+__device__ __forceinline__ Piece piece_at(const PagedAttnParams& p, const Line& ln, int pos, int align) {
   int lo = 0, hi = min(ln.nslot, p.B);             // last slot whose sum is <= pos: the one that holds pos
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -157,7 +168,7 @@ __device__ __forceinline__ Piece piece_at(const PagedAttnParams& p, const Line& 
   int base = ln.cum[lo];
   int b = lo * ln.per;
   for (int i = 0; i < ln.per; ++i, ++b) {          // one step when B is at most the thread count
-    c.s = seq_info<KEYS>(p, b);
+    c.s = seq_info<KEYS>(p, b, align);
     const int w = c.s.units * c.s.len;
     if (pos < base + w) break;
     base += w;
@@ -174,8 +185,8 @@ __device__ __forceinline__ Piece piece_at(const PagedAttnParams& p, const Line& 
   return c;
 }
 
-__device__ __forceinline__ int64_t part_slot(const PagedAttnParams& p, int cta, int which, int tile_rows) {
-  return (static_cast<int64_t>(cta) * 2 + which) * tile_rows;
+__device__ __forceinline__ int64_t part_slot(const PagedAttnParams& p, int cta, int which) {
+  return (static_cast<int64_t>(cta) * 2 + which) * p.rows;
 }
 
 // Where packed row r (node r / G, head r % G of kv head g) of sequence b goes.
@@ -198,9 +209,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 }  // namespace paged
 
 cudaError_t launch_attn_paged_simt(const PagedAttnParams& p, int grid, cudaStream_t stream);
-// Combines the split units' rows; tile_rows: rows of a partial's slot.
-cudaError_t launch_attn_paged_merge(const PagedAttnParams& p, int grid, int tile_rows, cudaStream_t stream);
+// Combines the split units' rows.
+cudaError_t launch_attn_paged_merge(const PagedAttnParams& p, int grid, cudaStream_t stream);
 bool attn_paged_tc_supported(const tv_attn_paged_args* a);
+// Rows of a unit of the tensor-core kernel, and its TMA boxes.
+int attn_paged_tc_rows(const tv_attn_paged_args* a);
+int attn_paged_tc_box(int page_size);
 cudaError_t launch_attn_paged_tc(const PagedAttnParams& p, int grid, cudaStream_t stream);
 // Query rows of the CUDA-core kernel's row tile and its CTAs per SM.
 int attn_paged_simt_rows(int64_t rows);

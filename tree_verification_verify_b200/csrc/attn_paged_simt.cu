@@ -75,11 +75,11 @@ attn_paged_simt_kernel(PagedAttnParams p, int vec) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wr = warp / WK, wk = warp % WK;
   const int G = p.G;
-  build_line<kKeys, kThreads>(p, ln);
+  build_line<kKeys, kThreads>(p, ln, 0);
   SplitUnit split = {-1, 0, 0, 0, 0};
 
   for (int pos = ln.first; pos < ln.last;) {
-    const Piece c = piece_at<kKeys>(p, ln, pos);
+    const Piece c = piece_at<kKeys>(p, ln, pos, 0);
     pos += c.t1 - c.t0;
     const int n = c.s.n, L = c.s.L;
     const int packed0 = c.rt * R;
@@ -260,7 +260,7 @@ attn_paged_simt_kernel(PagedAttnParams p, int vec) {
     }
     const bool whole = c.t0 == 0 && c.t1 == c.s.len;
     const int which = c.t0 == 0 ? 1 : 0;
-    const int64_t slot0 = part_slot(p, blockIdx.x, which, R);
+    const int64_t slot0 = part_slot(p, blockIdx.x, which);
     // the WK warps of a row share its rows' output
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -308,7 +308,7 @@ attn_paged_simt_kernel(PagedAttnParams p, int vec) {
 // A warp per row of a split unit:
 //   M = max lse, w = 2^(lse - M), out = sum w o / sum w, lse = M + log2 sum w
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) attn_paged_merge_kernel(PagedAttnParams p, int tile_rows) {
+__global__ void __launch_bounds__(kThreads) attn_paged_merge_kernel(PagedAttnParams p) {
   constexpr int DL = D / 32;
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const int r = blockIdx.y * kWarps + (threadIdx.x >> 5);
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_merge_kernel(PagedAttnPar
   float M = -INFINITY;
   bool bad = false;
   for (int k = c0 + lane; k <= u.c1; k += 32) {
-    const float v = p.part_lse[part_slot(p, k, k == c0, tile_rows) + r];
+    const float v = p.part_lse[part_slot(p, k, k == c0) + r];
     bad |= v != v;
     M = fmaxf(M, v);
   }
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_merge_kernel(PagedAttnPar
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int k = min(k0 + i, u.c1);
-        const int64_t s = part_slot(p, k, k == c0, tile_rows) + r;
+        const int64_t s = part_slot(p, k, k == c0) + r;
         v[i] = p.part_lse[s];
         const float* src = p.part_o + s * D + lane * DL;
         if (DL == 4) *reinterpret_cast<float4*>(o[i]) = *reinterpret_cast<const float4*>(src);
@@ -404,9 +404,9 @@ int attn_paged_simt_rows(int64_t rows) { return rows > 16 ? 32 : (rows > 8 ? 16 
 namespace {
 
 template <typename T, int D>
-cudaError_t merge(const PagedAttnParams& p, int grid, int tile_rows, cudaStream_t stream) {
+cudaError_t merge(const PagedAttnParams& p, int grid, cudaStream_t stream) {
   // The launch may overlap the first kernel's tail: every CTA waits for that kernel to end
-  const int most = static_cast<int>(std::min(static_cast<int64_t>(tile_rows), static_cast<int64_t>(p.T) * p.G));
+  const int most = static_cast<int>(std::min(static_cast<int64_t>(p.rows), static_cast<int64_t>(p.T) * p.G));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, (most + kWarps - 1) / kWarps);
   cfg.blockDim = dim3(kThreads);
@@ -416,23 +416,23 @@ cudaError_t merge(const PagedAttnParams& p, int grid, int tile_rows, cudaStream_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_paged_merge_kernel<T, D>, p, tile_rows);
+  return cudaLaunchKernelEx(&cfg, attn_paged_merge_kernel<T, D>, p);
 }
 
 template <typename T>
-cudaError_t merge_d(const PagedAttnParams& p, int grid, int tile_rows, cudaStream_t stream) {
+cudaError_t merge_d(const PagedAttnParams& p, int grid, cudaStream_t stream) {
   switch (p.d) {
-    case 32: return merge<T, 32>(p, grid, tile_rows, stream);
-    case 64: return merge<T, 64>(p, grid, tile_rows, stream);
-    default: return merge<T, 128>(p, grid, tile_rows, stream);
+    case 32: return merge<T, 32>(p, grid, stream);
+    case 64: return merge<T, 64>(p, grid, stream);
+    default: return merge<T, 128>(p, grid, stream);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_attn_paged_merge(const PagedAttnParams& p, int grid, int tile_rows, cudaStream_t stream) {
+cudaError_t launch_attn_paged_merge(const PagedAttnParams& p, int grid, cudaStream_t stream) {
   if (grid == 1) return cudaSuccess;                       // nothing is split
-  return p.dtype == TV_BF16 ? merge_d<__nv_bfloat16>(p, grid, tile_rows, stream) : merge_d<float>(p, grid, tile_rows, stream);
+  return p.dtype == TV_BF16 ? merge_d<__nv_bfloat16>(p, grid, stream) : merge_d<float>(p, grid, stream);
 }
 
 int attn_paged_simt_ctas(int, int d) { return d == 128 ? 2 : 4; }

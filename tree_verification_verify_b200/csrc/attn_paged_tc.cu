@@ -2,43 +2,46 @@
 // with d = 64 or 128.
 //
 // A persistent CTA per SM works through its stretch of the line
-// (attn_paged.cuh).  A unit's 128 query rows are the G heads of one kv head
-// of 128 / G nodes; its key tiles are 128 prefix rows, fetched page by page,
-// then tree nodes 128 at a time from the last ones down, masked per row by
-// the row's root path.  Loads, products and softmax of consecutive tiles
-// overlap across the borders of units: the producers run ahead into the next
-// unit while the softmax warps write the last one out.
+// (attn_paged.cuh).  A unit's query rows are the G heads of one kv head of
+// up to 128 / G nodes (one row tile), or of twice as many (PAIR: two row
+// tiles, so that every K/V tile serves 256 rows); its key tiles are 128
+// prefix rows, fetched page by page, then tree nodes 128 at a time from the
+// last ones down, masked per row by the row's root path.  The prefix's last
+// rows and a small tree share one tile.  Loads, products and softmax of
+// consecutive tiles overlap across the borders of units.
 //
 // Warp roles (384 threads):
-//   warps 0-7  softmax and output: two warpgroups of a thread per query row
-//              (TMEM lane) take the tiles in turn, each with an online
-//              softmax state and an accumulator (O_0, O_1 in TMEM) of its
-//              own that meet once per piece.  One group's exponentials run
-//              while the other waits for TMEM and barriers (about 2000 of
-//              the 5000 cycles of a tile when both worked on halves of the
-//              same tile).  Warps without a valid row skip the arithmetic
-//              (decoding: G of 128 rows are real);
+//   warps 0-7  softmax and output: two warpgroups, a thread per query row
+//              (TMEM lane), each with an online softmax state and an
+//              accumulator of its own (O_0, O_1 in TMEM).  With one row tile
+//              they take the key tiles in turn and meet once per piece;
+//              with two (PAIR) group h has row tile h.  One group's
+//              exponentials run while the other waits for TMEM and barriers
+//              (both on halves of the same tile: 5000 cycles a tile, half of
+//              them waits; in turn: 2700).  Warps without a valid row skip
+//              the arithmetic (decoding: G of 128 rows are real);
 //   warp 8     K tiles, warp 10 V tiles.  Page sizes that are multiples of
 //              8 rows: one TMA box per run of rows that both the page and
 //              the tile divide into (gcd(page size, 128) rows), a box per
 //              lane; the page table is read for several tiles at a time, one
 //              batch ahead.  Other page sizes: 16-byte cp.async per row
 //              into the same swizzled layout;
-//   warp 9     MMA: one thread polls what is ready and issues S = Q K^T two
-//              tiles ahead or O_h += P V (P read from TMEM), so neither
+//   warp 9     MMA: one thread polls what is ready and issues S = Q K^T up
+//              to two ahead or O_h += P V (P read from TMEM), so neither
 //              waits for the other's operands;
-//   warp 11    Q of the next unit, and parent[] for the tree tiles.
+//   warp 11    the pieces' descriptions, several ahead of their use (finding
+//              one takes a search and four divisions), Q and parent[].
 // Online softmax in base 2; O is rescaled only when a row's maximum grows by
-// more than 2^8 (P <= 256, exact in O / l).  P is rounded to bf16
-// for the product with V (the tensor cores' operand type); sums use the
-// unrounded fp32 weights.
+// more than 2^8 (P <= 256, exact in O / l).  P is rounded to bf16 for the
+// product with V (the tensor cores' operand type); sums use the unrounded
+// fp32 weights.
 //
 // V of a tree tile may hold infinities or NaN in nodes that a row does not
-// see, and 0 * NaN would reach that row.  The softmax warps look the tile
-// over, put 0 in such places and note them; a row that does see one adds
-// those values to its output at the end (an infinity or a NaN takes over
-// whatever its weight).  Rows of a tile past the prefix or past n_nodes are
-// cleared the same way.
+// see, and 0 * NaN would reach that row.  The softmax warps look the nodes'
+// rows over, put 0 in such places and note the rows; a query row that sees
+// one adds those values to its output at the end (an infinity or a NaN takes
+// over whatever its weight).  Rows of the last K steps that are no keys are
+// cleared; later K steps are not issued.
 // Every mbarrier wait is bounded: on expiry the CTA records TV_DEV_TIMEOUT,
 // drains what it issued, frees its TMEM, and its rows come out as NaN.
 #include <cuda.h>
@@ -60,32 +63,83 @@ constexpr int kSoftmaxThreads = 256;
 constexpr int kWarpK = 8, kWarpMma = 9, kWarpV = 10, kWarpTree = 11;
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kMaxT = 2048;
+constexpr int kTreeBox = 8;                               // tree nodes of a TMA box
 constexpr uint32_t kHalfBytes = kRows * 128;              // 128 rows x 64 bf16
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;                // S buffers 128 apart, O_0 and O_1 128 apart
 constexpr uint16_t kRootMark = 0xFFFEu, kBadMark = 0xFFFFu;
+constexpr int kRing = 8, kAhead = 3;                      // descriptions kept, and made ahead
 
-template <int D>
+// Shared memory: Q, the K and V rings, two parent[] buffers.  192 KB of
+// tiles: 96 KB of K (64 KB where there are two Q tiles) and 64 KB of V.
+template <int D, bool PAIR>
 struct Shape {
   static constexpr uint32_t kTile = D / 64 * kHalfBytes;  // bytes of a K, V or Q tile
-  static constexpr int kKS = 3 * 128 / D, kVS = 2 * 128 / D;   // ring stages: 96 KB of K, 64 KB of V
-  static constexpr uint32_t kQ = 0, kK = kTile, kV = kK + kKS * kTile, kPar = kV + kVS * kTile;
+  static constexpr int kKS = (PAIR ? 2 : 3) * 128 / D, kVS = 2 * 128 / D;
+  static constexpr uint32_t kQ = 0, kK = (PAIR ? 2 : 1) * kTile, kV = kK + kKS * kTile, kPar = kV + kVS * kTile;
   static constexpr uint32_t kBytes = kPar + 2 * kMaxT * 2;
+};
+
+// A piece, ready for use: its tiles are na prefix tiles from a0 on, then ntr
+// tree tiles whose first nodes are lo0, lo0 - 128, ...
+struct Desc {
+  int valid;                    // 0: there are no more pieces
+  int cnt;                      // na + ntr
+  int index, queue;             // pieces before it, and those of them with tiles
+  int b, g, i0;                 // sequence, kv head, first node
+  int nodes;                    // nodes of the unit
+  int n, L;                     // the sequence's nodes and prefix rows
+  int a0, na, ntr, lo0;
+  int rem, off;                 // the tree tile's prefix rows, and where its nodes begin
+  int bad_len, whole, begins;
+  int c1;                       // the CTA in which the unit ends
+  __device__ __forceinline__ int live_end(int r) const {   // rows of tile r up to the last key
+    if (r < na) return min(kKeys, L - (a0 + r) * kKeys);
+    return off + min(n - (lo0 - (r - na) * kKeys), kKeys - off);
+  }
 };
 
 struct Bars {
   uint64_t q_full, q_empty;
   uint64_t k_full[6], k_empty[6], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_full[2], pv_done[2];              // by tile parity: S buffer, warpgroup, accumulator
-  uint64_t o_free;                                        // a piece's accumulators have been read
+  uint64_t s_full[2], p_full[2], pv_done[2];              // by group: S buffer, P, accumulator
+  uint64_t o_free[2];                                     // the accumulator of the last piece has been read
   uint64_t t_full[2], t_empty[2];                         // parent[] buffers
+  uint64_t w_full[kRing], w_empty[kRing];                 // piece descriptions
+  uint64_t vfix;                                          // PAIR: group 0 has looked a tree tile over
   uint32_t tmem_base;
   int abort;
   int bad_piece[8];                                       // piece number + 1 that met a bad page
-  uint32_t vbad[2][2][4];                                 // [group][its tile parity] V rows with infinities or NaN
+  uint32_t vbad[2][4][4];                                 // [group][its tree tile & 3] V rows with infinities or NaN
+  Desc desc[kRing];
   float red_m[2][kRows], red_l[2][kRows];
   uint8_t red_nf[2][kRows];
 };
+
+// Two fp32 operations in one instruction (sm_100).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
@@ -116,85 +170,25 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
   tmem_st16u(taddr, u);
 }
 
-// The real tiles of a piece: prefix tiles [a0, a1), tree tiles [b0, b1)
-// (tree tiles of later nodes than the row tile's are left out).
-struct Tiles {
-  int a0, a1, b0, b1;
-  __device__ __forceinline__ int count() const { return a1 - a0 + b1 - b0; }
-};
-
-__device__ __forceinline__ Tiles tiles_of(const Piece& c, int node_hi) {
-  Tiles t;
-  t.a0 = min(c.t0, c.s.nprefix);
-  t.a1 = min(c.t1, c.s.nprefix);
-  const int skip = c.s.ntree > 0 ? c.s.ntree - (node_hi / kKeys + 1) : 0;
-  t.b1 = min(c.t1, c.s.nprefix + c.s.ntree);
-  t.b0 = max(c.t0, c.s.nprefix + skip);
-  t.b1 = max(t.b0, t.b1);
-  return t;
-}
-
 }  // namespace ptc
 
 using namespace ptc;
 
-// Walks a CTA's pieces; every role has its own.
-struct PieceWalk {
-  int pos;
-  int index;                    // pieces before this one
-  int queue;                    // of those, pieces with tiles
-  Piece c;
-  Tiles t;
-  int i0, nodes, cnt;
-  __device__ __forceinline__ void start(const Line& ln) { pos = ln.first; index = -1; queue = -1; cnt = 0; }
-  __device__ __forceinline__ bool next(const PagedAttnParams& p, const Line& ln) {
-    if (pos >= ln.last) return false;
-    c = piece_at<kKeys>(p, ln, pos);
-    pos += c.t1 - c.t0;
-    const int npt = p.rows / p.G;
-    i0 = c.rt * npt;
-    nodes = min(npt, c.s.n - i0);
-    t = tiles_of(c, i0 + nodes - 1);
-    cnt = t.count();
-    ++index;
-    queue += cnt > 0;
-    return true;
-  }
-};
-
-// The MMA thread needs a piece's tile count alone.
-struct CountWalk {
-  int pos, queue, cnt;
-};
-__device__ __forceinline__ bool next_count(const PagedAttnParams& p, const Line& ln, CountWalk& x) {
-  PieceWalk w;
-  w.pos = x.pos;
-  w.index = 0;
-  w.queue = x.queue;
-  do {
-    if (!w.next(p, ln)) return false;
-  } while (w.cnt == 0);
-  x.pos = w.pos;
-  x.queue = w.queue;
-  x.cnt = w.cnt;
-  return true;
-}
-
-template <int D>
+template <int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_kt,
-                     const __grid_constant__ CUtensorMap map_vt, PagedAttnParams p, int box) {
-  using Sh = Shape<D>;
+                     const __grid_constant__ CUtensorMap map_vt, PagedAttnParams p) {
+  using Sh = Shape<D, PAIR>;
   constexpr int KS = Sh::kKS, VS = Sh::kVS;
   constexpr uint32_t TB = Sh::kTile;
-  constexpr int DH = D / 2;                               // output columns of a half
   extern __shared__ uint8_t dsmem_raw[];
   __shared__ Bars bars;
   __shared__ Line ln;
-  __shared__ PieceWalk walks[kSoftmaxThreads / 32];       // the softmax warps': registers are for scores
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int G = p.G;
+  const int G = p.G, box = p.box;
+  const int align = box > 0 ? box : 8;
+  const int npt = (PAIR ? p.rows / 2 : p.rows) / G;       // nodes of a row tile
   const uint32_t raw = smem_u32(dsmem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;           // 128B swizzle atoms are 1 KB
   uint8_t* gbase = dsmem_raw + (base - raw);
@@ -213,10 +207,12 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       mbar_init(&bars.s_full[s], 1);
       mbar_init(&bars.p_full[s], 4);
       mbar_init(&bars.pv_done[s], 1);
+      mbar_init(&bars.o_free[s], PAIR ? 4 : 8);           // PAIR: a group reads its own accumulator alone
       mbar_init(&bars.t_full[s], 1); mbar_init(&bars.t_empty[s], 8);
-      for (int i = 0; i < 8; ++i) bars.vbad[s][i >> 2][i & 3] = 0;
+      for (int i = 0; i < 16; ++i) bars.vbad[s][i >> 2][i & 3] = 0;
     }
-    mbar_init(&bars.o_free, 8);
+    for (int s = 0; s < kRing; ++s) { mbar_init(&bars.w_full[s], 1); mbar_init(&bars.w_empty[s], 11); }
+    mbar_init(&bars.vfix, 4);
     for (int i = 0; i < 8; ++i) bars.bad_piece[i] = 0;
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -229,11 +225,22 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
-  build_line<kKeys, kThreads>(p, ln);                     // ends with a CTA barrier
+  build_line<kKeys, kThreads>(p, ln, align);              // ends with a CTA barrier
   fence_after();
   const uint32_t tmem = bars.tmem_base;
-  PieceWalk w;
-  w.start(ln);
+
+  // Description k, and its release (every consuming warp once per piece; the
+  // wait ignores the abort flag: after an abort every role still walks the
+  // pieces to the end, so that all rows are written)
+  auto desc = [&](int k) -> const Desc* {
+    if (!mbar_wait_cluster(&bars.w_full[k % kRing], (k / kRing) & 1)) {
+      *abort = 1;
+      return nullptr;
+    }
+    const Desc* d = &bars.desc[k % kRing];
+    return d->valid ? d : nullptr;
+  };
+  auto release = [&](int k) { mbar_arrive(&bars.w_empty[k % kRing]); };
 
   // 384 threads launch with 168 registers: 256 softmax threads take 208, the
   // other 128 keep 88 (256 * 208 + 128 * 88 = 384 * 168)
@@ -251,12 +258,15 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     int it = 0;
     bool ok = true;
     int pending = -1;                                     // stage whose cp.async copies are not announced yet
+    auto announce = [&](int s) {                          // copies that have landed, to the tensor cores
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
+    };
     auto flush = [&]() {
       if (pending < 0) return;
       cp_async_wait_all();
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[pending]);
+      announce(pending);
       pending = -1;
     };
     auto acquire = [&](int s) -> bool {                   // the stage is free
@@ -267,27 +277,33 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       if (lane == 0) a = mbar_wait(&empty[s], ((it / NS) - 1) & 1, abort);
       return __all_sync(0xffffffffu, a);
     };
-    auto bad_page = [&]() { if (isk) bars.bad_piece[w.index & 7] = w.index + 1; };
-    while (ok && w.next(p, ln)) {
-      const int32_t* table = p.table + w.c.b * p.pt_sb;
-      const int L = w.c.s.L, g = w.c.g, b = w.c.b;
+    for (int k = 0;; ++k) {
+      const Desc* d = desc(k);
+      if (!d) break;
+      const int32_t* table = p.table + d->b * p.pt_sb;
+      const int L = d->L, g = d->g, b = d->b, a0 = d->a0, a1 = d->a0 + d->na, cnt = d->cnt;
+      const int rem = d->rem, off = d->off, nodes = d->n, lo0 = d->lo0, index = d->index;
+      auto bad_page = [&]() { if (isk) bars.bad_piece[index & 7] = index + 1; };
       if (box > 0) {
-        // lane l holds the run of `box` rows number l % nb of tile l / nb of a batch of 32 / nb tiles
+        // lane l holds the run of `box` rows number l % nb of tile l / nb of
+        // a batch of 32 / nb tiles; the tile after the last prefix tile may
+        // hold the prefix's last rows
         const int nb = kKeys / box, batch = 32 / nb;
+        const int stop = a1 + (rem > 0);
         int row = 0, page = 0, row_n = 0, page_n = 0;
         auto look = [&](int t, int& r, int& pg) {
           const unsigned pos = static_cast<unsigned>(t + lane / nb) * kKeys + lane % nb * box;
           r = -1;
           pg = 0;
-          if (t + lane / nb < w.t.a1 && pos < static_cast<unsigned>(L)) {
+          if (t + lane / nb < stop && pos < static_cast<unsigned>(L)) {
             r = static_cast<int>(pos % P);
             pg = __ldg(table + pos / P);
           }
         };
-        look(w.t.a0, row_n, page_n);
-        for (int t = w.t.a0; ok && t < w.t.a1; ++t, ++it) {
-          const int k = (t - w.t.a0) % batch;
-          if (k == 0) {
+        look(a0, row_n, page_n);
+        for (int r = 0; ok && r < cnt; ++r, ++it) {
+          const int t = a0 + r, q = r % batch;
+          if (q == 0) {
             row = row_n;
             page = page_n;
             look(t + batch, row_n, page_n);
@@ -295,76 +311,76 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           const int s = it % NS;
           ok = acquire(s);
           if (!ok) break;
-          const bool mine = lane / nb == k && row >= 0;
+          const bool mine = lane / nb == q && row >= 0;
           if (mine && (page < 0 || page >= p.num_pages)) {
             bad_page();
             page = p.num_pages;                           // past the pool's end: the box reads as zeros
           }
-          const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+          uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine))) * box * D * 2;
+          // tree nodes: boxes of 8 into rows off, off + 8, ...
+          const int lo = lo0 - (t - a1) * kKeys;
+          const int tb = t >= a1 ? (min(nodes - lo, kKeys - off) + kTreeBox - 1) / kTreeBox : 0;
+          bytes += static_cast<uint32_t>(tb) * kTreeBox * D * 2;
           __syncwarp();                                   // a bad page is noted before the tile is announced
-          if (lane == 0) mbar_expect_tx(&full[s], static_cast<uint32_t>(boxes) * box * D * 2);
+          if (lane == 0) mbar_expect_tx(&full[s], bytes);
           __syncwarp();
-          if (mine) {
-            const uint32_t dst = ring + s * TB + lane % nb * box * 128;
+          const uint32_t dst = ring + s * TB;
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) tma_load_4d(map, dst + h * kHalfBytes, &full[s], 64 * h, g, row, page);
+          for (int h = 0; h < D / 64; ++h) {
+            if (mine) tma_load_4d(map, dst + lane % nb * box * 128 + h * kHalfBytes, &full[s], 64 * h, g, row, page);
+            if (lane < tb)
+              tma_load_4d(map_tree, dst + (off + lane * kTreeBox) * 128 + h * kHalfBytes, &full[s], 64 * h, g,
+                          lo + lane * kTreeBox, b);
           }
         }
       } else {
         const char* pool = static_cast<const char*>(isk ? p.kp : p.vp) + g * p.kv_sh * 2;
-        for (int t = w.t.a0; ok && t < w.t.a1; ++t, ++it) {
-          // lane l holds the places of rows l, l + 32, l + 64, l + 96
-          int64_t off[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const unsigned pos = static_cast<unsigned>(t) * kKeys + i * 32 + lane;
-            off[i] = -1;
-            if (pos < static_cast<unsigned>(L)) {
-              const int page = __ldg(table + pos / P);
-              if (page < 0 || page >= p.num_pages) bad_page();
-              else off[i] = (page * p.kv_sp + static_cast<int64_t>(pos % P) * p.kv_sr) * 2;
-            }
-          }
+        const char* tree = static_cast<const char*>(isk ? p.kt : p.vt) + (b * p.kt_sb + g * p.kt_sh) * 2;
+        for (int r = 0; ok && r < cnt; ++r, ++it) {
+          // lane l looks up rows l, l + 32, l + 64, l + 96: the byte offset in
+          // its source and, in bit 0, which source; -2: no row
+          const int t = a0 + r, lo = lo0 - (t - a1) * kKeys;
+          const int np = t < a1 ? kKeys : rem;            // prefix rows (as far as the prefix goes)
           const int s = it % NS;
-          ok = acquire(s);
-          if (!ok) break;
           constexpr int CPR = D / 8, RPI = 32 / CPR;      // 16-byte chunks of a row, rows of a step
           const int ch = lane % CPR;
           const uint32_t dst = ring + s * TB + ch / 8 * kHalfBytes;
+          int64_t o[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-#pragma unroll 8
-            for (int r0 = 0; r0 < 32; r0 += RPI) {
-              const int r = r0 + lane / CPR;
-              const int64_t o = __shfl_sync(0xffffffffu, off[i], r);
-              const int rr = i * 32 + r;
-              if (o >= 0) cp_async16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), pool + o + ch * 16);
+            const int x = i * 32 + lane;
+            o[i] = -2;
+            const unsigned pos = static_cast<unsigned>(t) * kKeys + x;
+            if (x < np && pos < static_cast<unsigned>(L)) {
+              const int page = __ldg(table + pos / P);
+              if (page < 0 || page >= p.num_pages) bad_page();
+              else o[i] = (page * p.kv_sp + static_cast<int64_t>(pos % P) * p.kv_sr) * 2;
+            } else if (t >= a1 && x >= off && lo + x - off < nodes) {
+              o[i] = static_cast<int64_t>(lo + x - off) * p.kt_st * 2 + 1;
             }
           }
-          const int before = pending;
+          ok = acquire(s);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll 4
+            for (int r0 = 0; r0 < 32; r0 += RPI) {
+              const int64_t y = __shfl_sync(0xffffffffu, o[i], r0 + lane / CPR);
+              const int rr = i * 32 + r0 + lane / CPR;
+              if (y >= 0)
+                cp_async16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), ((y & 1) ? tree + (y - 1) : pool + y) + ch * 16);
+            }
+          }
           asm volatile("cp.async.commit_group;" ::: "memory");
-          if (before >= 0) {                              // the tile before this one has landed
+          if (pending >= 0) {                             // the tile before this one has landed
             asm volatile("cp.async.wait_group 1;" ::: "memory");
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[before]);
+            announce(pending);
           }
           pending = s;
         }
       }
-      for (int t = w.t.b0; ok && t < w.t.b1; ++t, ++it) {
-        const int s = it % NS;
-        ok = acquire(s);
-        if (!ok) break;
-        flush();
-        if (lane == 0) {
-          const int lo = (w.c.s.ntree - 1 - (t - w.c.s.nprefix)) * kKeys;
-          mbar_expect_tx(&full[s], TB);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(map_tree, ring + s * TB + h * kHalfBytes, &full[s], 64 * h, g, lo, b);
-        }
-      }
+      __syncwarp();
+      if (lane == 0) release(k);
     }
     flush();
     // drain: every issued load lands before the CTA can exit
@@ -372,37 +388,83 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       for (int j = (it > NS ? it - NS : 0); j < it; ++j) mbar_drain(&full[j % NS], (j / NS) & 1);
     __syncwarp();
   } else if (warp == kWarpTree) {
-    // ------------------------------------------------------------ Q and parent[]
-    int nq = 0, ntree = 0;
-    bool ok = true;
-    auto load_q = [&]() -> bool {
-      bool a = true;
-      if (nq > 0) {
-        if (lane == 0) a = mbar_wait(&bars.q_empty, (nq - 1) & 1, abort);
-        a = __all_sync(0xffffffffu, a);
+    // ------------------------------------------------------------ pieces, Q and parent[]
+    int nq = 0, ntree = 0, made = 0, queue = 0, pos = ln.first;
+    bool ok = true, more = true;
+    auto make = [&]() {                                   // description number `made`
+      const int s = made % kRing;
+      if (made >= kRing) {
+        bool a = true;
+        if (lane == 0) a = mbar_wait_cluster(&bars.w_empty[s], ((made / kRing) - 1) & 1);
+        if (!__all_sync(0xffffffffu, a)) { *abort = 1; more = false; return; }
       }
-      if (!a) return false;
+      Desc x;
+      x.valid = pos < ln.last;
+      more = x.valid;
+      if (x.valid) {
+        const Piece c = piece_at<kKeys>(p, ln, pos, align);
+        pos += c.t1 - c.t0;
+        const int npu = PAIR ? 2 * npt : npt;             // nodes of a unit
+        x.b = c.b; x.g = c.g; x.i0 = c.rt * npu;
+        x.nodes = min(npu, c.s.n - x.i0);
+        x.n = c.s.n; x.L = c.s.L;
+        x.a0 = min(c.t0, c.s.nprefix);
+        x.na = min(c.t1, c.s.nprefix) - x.a0;
+        // tree tiles of later nodes than the unit's are left out
+        const int skip = c.s.ntree > 0 ? c.s.ntree - ((x.i0 + x.nodes - 1) / kKeys + 1) : 0;
+        const int b0 = max(c.t0, c.s.nprefix + skip), b1 = min(c.t1, c.s.nprefix + c.s.ntree);
+        x.ntr = max(0, b1 - b0);
+        x.lo0 = (c.s.ntree - 1 - (b0 - c.s.nprefix)) * kKeys;
+        x.rem = x.ntr > 0 ? c.s.rem : 0;
+        x.off = x.ntr > 0 ? c.s.off : 0;
+        x.cnt = x.na + x.ntr;
+        x.index = made;
+        x.queue = queue;
+        queue += x.cnt > 0;
+        x.bad_len = c.s.bad_len;
+        x.whole = c.t0 == 0 && c.t1 == c.s.len;
+        x.begins = c.t0 == 0;
+        x.c1 = (c.unit_first + c.s.len - 1) / ln.step;
+      }
       if (lane == 0) {
-        mbar_expect_tx(&bars.q_full, static_cast<uint32_t>(p.rows) * D * 2);
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-          tma_load_4d(&map_q, base + Sh::kQ + h * kHalfBytes, &bars.q_full, 64 * h, w.c.g * G, w.i0, w.c.b);
+        bars.desc[s] = x;
+        mbar_arrive(&bars.w_full[s]);
       }
-      ++nq;
-      return true;
+      __syncwarp();
+      ++made;
     };
-    while (ok && w.next(p, ln)) {
-      if (w.cnt == 0) continue;
+    for (int k = 0;; ++k) {
+      while (more && made <= k + kAhead) make();
+      if (k >= made) break;
+      const Desc& d = bars.desc[k % kRing];               // (kept: this warp makes its successor in the ring)
+      if (!d.valid) break;
+      if (d.cnt == 0 || !ok) continue;
+      auto load_q = [&]() {
+        bool a = true;
+        if (nq > 0 && lane == 0) a = mbar_wait(&bars.q_empty, (nq - 1) & 1, abort);
+        ok = __all_sync(0xffffffffu, a);
+        if (!ok) return;
+        if (lane == 0) {
+          // rows past the tensor's nodes read as zeros
+          mbar_expect_tx(&bars.q_full, static_cast<uint32_t>(p.rows) * D * 2);
+#pragma unroll
+          for (int q = 0; q < (PAIR ? 2 : 1); ++q)
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_4d(&map_q, base + Sh::kQ + q * TB + h * kHalfBytes, &bars.q_full, 64 * h, d.g * G, d.i0 + q * npt, d.b);
+        }
+        ++nq;
+      };
       const bool first = nq == 0;
-      if (first) ok = load_q();
-      if (ok && w.t.b1 > w.t.b0) {
+      if (first) load_q();
+      if (ok && d.ntr > 0) {
         const int buf = ntree & 1;
         bool a = true;
         if (ntree >= 2 && lane == 0) a = mbar_wait(&bars.t_empty[buf], ((ntree >> 1) - 1) & 1, abort);
         ok = __all_sync(0xffffffffu, a);
-        if (!ok) break;
-        const int32_t* par = p.parent + w.c.b * p.par_sb;
-        for (int j = lane; j < w.i0 + w.nodes; j += 32) {
+        if (!ok) continue;
+        const int32_t* par = p.parent + d.b * p.par_sb;
+        for (int j = lane; j < d.i0 + d.nodes; j += 32) {
           const int pj = par[j];
           spar[buf * kMaxT + j] = j == 0 ? (pj == -1 ? kRootMark : kBadMark)
                                          : ((pj >= 0 && pj < j) ? static_cast<uint16_t>(pj) : kBadMark);
@@ -411,68 +473,81 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (lane == 0) mbar_arrive(&bars.t_full[buf]);
         ++ntree;
       }
-      if (ok && !first) ok = load_q();
+      if (ok && !first) load_q();
     }
     if (lane == 0 && nq > 0) mbar_drain(&bars.q_full, (nq - 1) & 1);
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
+      constexpr int SUB = PAIR ? 2 : 1;                   // products of a kind per key tile
       const uint32_t idesc_qk = instr_desc(kRows, kKeys, 0, 0);
       const uint32_t idesc_pv = instr_desc(kRows, D, 0, 1);
-      CountWalk cs = {ln.first, -1, 0}, cp = cs;          // the pieces of the next S and of the next P V
-      int rs = 0, rp = 0;                                 // tiles done in those pieces
-      int is = 0, ip = 0;                                 // S and P V issued in all
-      bool more_s = next_count(p, ln, cs), more_p = more_s;
-      cp = cs;
-      auto step = [&](CountWalk& x, int& r, bool& more) {
-        if (r >= x.cnt) {
-          more = next_count(p, ln, x);
-          r = 0;
-        }
+      int is = 0, ip = 0;                                 // S and P V issued in all; number i is of group i & 1
+      int rs = 0, rp = 0;                                 // of those, in the present pieces
+      int ks = -1, kp = -1;                               // the present pieces
+      const Desc *ds = nullptr, *dp = nullptr;
+      auto next_s = [&]() { do ds = desc(++ks); while (ds && ds->cnt == 0); rs = 0; };
+      auto next_p = [&]() {
+        do {
+          if (kp >= 0) release(kp);
+          dp = desc(++kp);
+        } while (dp && dp->cnt == 0);
+        rp = 0;
       };
+      next_s();
+      next_p();
       uint32_t idle = 0;
-      while (more_p) {
+      while (dp) {
         // all tests of a poll are independent: together they cost little more than one
-        const bool want_s = more_s && is < ip + 2;
-        const bool tk = want_s && mbar_test(&bars.k_full[is % KS], (is / KS) & 1);
-        const bool tq = want_s && (rs > 0 || mbar_test(&bars.q_full, cs.queue & 1));
+        const int tks = is / SUB, tvs = ip / SUB;
+        const bool want_s = ds && is < ip + 2;
+        const bool tk = want_s && mbar_test(&bars.k_full[tks % KS], (tks / KS) & 1);
+        const bool tq = want_s && (rs > 0 || mbar_test(&bars.q_full, ds->queue & 1));
         const bool want_p = ip < is;
-        const bool tv = want_p && mbar_test(&bars.v_full[ip % VS], (ip / VS) & 1);
+        const bool tv = want_p && mbar_test(&bars.v_full[tvs % VS], (tvs / VS) & 1);
         const bool tp = want_p && mbar_test(&bars.p_full[ip & 1], (ip >> 1) & 1);
-        // the first tile of either group overwrites its accumulator, so the last piece's must have been read
-        const bool to = want_p && (rp > 1 || cp.queue == 0 || mbar_test(&bars.o_free, (cp.queue - 1) & 1));
+        // the first product of either group overwrites its accumulator, so the last piece's must have been read
+        const bool to = want_p && (rp > 1 || dp->queue == 0 || mbar_test(&bars.o_free[ip & 1], (dp->queue - 1) & 1));
         bool did = false;
         if (tk && tq) {
           fence_after();
-          const uint32_t sq = base + Sh::kQ, sk = base + Sh::kK + (is % KS) * TB;
+          const uint32_t sq = base + Sh::kQ + (PAIR ? (is & 1) * TB : 0), sk = base + Sh::kK + (tks % KS) * TB;
           const uint32_t sd = tmem + kColS + (is & 1) * 128;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-            mma_bf16(sd, smem_desc(sq + off, 16, 1024), smem_desc(sk + off, 16, 1024), idesc_qk, kk > 0);
+            const uint32_t o = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+            mma_bf16(sd, smem_desc(sq + o, 16, 1024), smem_desc(sk + o, 16, 1024), idesc_qk, kk > 0);
           }
-          mma_commit(&bars.k_empty[is % KS]);
+          if (!PAIR || (is & 1)) mma_commit(&bars.k_empty[tks % KS]);
           mma_commit(&bars.s_full[is & 1]);
-          if (rs == cs.cnt - 1) mma_commit(&bars.q_empty);
           ++is;
-          ++rs;
-          step(cs, rs, more_s);
+          if (++rs == ds->cnt * SUB) {
+            mma_commit(&bars.q_empty);
+            next_s();
+          }
           did = true;
         }
         // O_h += P V: P is bf16 pairs over the first 64 columns of its S
         if (tv && tp && to) {
           fence_after();
-          const uint32_t sv = base + Sh::kV + (ip % VS) * TB;
+          const uint32_t sv = base + Sh::kV + (tvs % VS) * TB;
+          const uint32_t od = tmem + kColO + (ip & 1) * 128, pd = tmem + kColS + (ip & 1) * 128;
+          const int steps = (dp->live_end(rp / SUB) + 15) / 16;
+          if (steps == 8) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tmem + kColO + (ip & 1) * 128, tmem + kColS + (ip & 1) * 128 + kk * 8,
-                        smem_desc(sv + kk * 2048, kHalfBytes, 1024), idesc_pv, (rp > 1 || kk > 0) ? 1u : 0u);
-          mma_commit(&bars.v_empty[ip % VS]);
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ts(od, pd + kk * 8, smem_desc(sv + kk * 2048, kHalfBytes, 1024), idesc_pv,
+                          (rp > 1 || kk > 0) ? 1u : 0u);
+          } else {
+            for (int kk = 0; kk < steps; ++kk)
+              mma_bf16_ts(od, pd + kk * 8, smem_desc(sv + kk * 2048, kHalfBytes, 1024), idesc_pv,
+                          (rp > 1 || kk > 0) ? 1u : 0u);
+          }
+          if (!PAIR || (ip & 1)) mma_commit(&bars.v_empty[tvs % VS]);
           mma_commit(&bars.pv_done[ip & 1]);
           ++ip;
-          ++rp;
-          step(cp, rp, more_p);
+          if (++rp == dp->cnt * SUB) next_p();
           did = true;
         }
         if (did) {
@@ -486,6 +561,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         // what was issued completes before the TMEM is freed
         for (int j = is > 2 ? is - 2 : 0; j < is; ++j) mbar_drain(&bars.s_full[j & 1], (j >> 1) & 1);
         for (int j = ip > 2 ? ip - 2 : 0; j < ip; ++j) mbar_drain(&bars.pv_done[j & 1], (j >> 1) & 1);
+        while (dp) next_p();
       }
     }
     __syncwarp();
@@ -497,143 +573,100 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t scol = trow + kColS + 128u * static_cast<uint32_t>(half);
     const uint32_t ocol = trow + kColO + 128u * static_cast<uint32_t>(half);
-    int it0 = 0, ntree = 0;                               // tiles before this piece
+    int it0 = 0, ntree = 0, nfix = 0;                     // tiles, tree pieces, tree tiles of the group before this piece
     SplitUnit split = {-1, 0, 0, 0, 0};
     bool ok = true;
-    PieceWalk& sw = walks[warp];
-    sw = w;
-    __syncwarp();
-    while (true) {
-      {
-        PieceWalk x = sw;
-        __syncwarp();
-        if (!x.next(p, ln)) break;
-        sw = x;
-        __syncwarp();
-      }
-      const PieceWalk& w = sw;
-      const Piece& c = w.c;
-      const int rows_here = w.nodes * G;
-      const bool live = (warp & 3) * 32 < rows_here;      // the warp has valid rows
-      const bool row_valid = row < rows_here;
-      const int my_node = w.i0 + row / G;
-      const int na = w.t.a1 - w.t.a0, cnt = w.cnt, nodes = c.s.n;
-      const int keys0 = c.s.L - w.t.a0 * kKeys;           // prefix keys from the piece's first tile on
-      const int lo0 = (c.s.ntree - 1 - (w.t.b0 - na - c.s.nprefix)) * kKeys;
-      const int r0 = (half ^ it0) & 1;                    // the group's first tile
+    for (int k = 0;; ++k) {
+      const Desc* d = desc(k);
+      if (!d) break;
+      const int first = PAIR ? half * npt : 0;            // the group's first node of the unit
+      const int my_rows = min(PAIR ? npt : p.rows / G, d->nodes - first) * G;
+      const bool live = (warp & 3) * 32 < my_rows;        // the warp has valid rows
+      const bool row_valid = row < my_rows;
+      const int my_node = d->i0 + first + row / G;
+      const int na = d->na, cnt = d->cnt, nodes = d->n, rem = d->rem, off = d->off, lo0 = d->lo0;
+      const int keys0 = d->L - d->a0 * kKeys;             // prefix keys from the piece's first tile on
+      const int r0 = PAIR ? 0 : (half ^ it0) & 1;         // the group's first tile
       float m_run = -INFINITY, l_run = 0.f;
       bool my_ok = true, nf = false;
       int cur = -2;                                       // walk position on this row's root path (-2: not begun)
       const uint16_t* par = spar + (ntree & 1) * kMaxT;
-      for (int r = r0; r < cnt; r += 2) {
+      for (int r = r0; r < cnt; r += PAIR ? 1 : 2) {
         const int it = it0 + r;
+        const uint32_t phase = static_cast<uint32_t>(PAIR ? it : it >> 1) & 1u;
         const bool tree = r >= na;
-        const int lo = lo0 - r * kKeys;                   // tree tile: its first node
-        const int nk = min(kKeys, tree ? nodes - lo : keys0 - r * kKeys);
-        const bool full = !tree && nk == kKeys;
+        const int lo = lo0 - (r - na) * kKeys;            // tree tile: its first node
+        // keys [0, np) of the prefix, [off, end) of the tree
+        const int np = tree ? rem : min(kKeys, keys0 - r * kKeys);
+        const int end = tree ? off + min(nodes - lo, kKeys - off) : np;
+        const bool full = np == kKeys;
         // keys that the row sees
         uint32_t mk[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (!full) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int nh = np - 32 * i;
+            mk[i] = nh >= 32 ? 0xffffffffu : (nh <= 0 ? 0u : ((1u << nh) - 1u));
+          }
+        }
         if (tree) {
           if (cur == -2) {
             ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.t_full[ntree & 1], (ntree >> 1) & 1, abort));
             cur = row_valid && ok ? my_node : -1;
           }
-          mk[0] = mk[1] = mk[2] = mk[3] = 0u;
           while (cur >= lo) {
-            const int k = cur - lo;
+            const int x = cur - lo + off;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mk[i] |= (k >> 5) == i ? 1u << (k & 31) : 0u;
+            for (int i = 0; i < 4; ++i) mk[i] |= (x >> 5) == i ? 1u << (x & 31) : 0u;
             const uint16_t up = par[cur];
             my_ok = my_ok && up != kBadMark;
             cur = up >= kRootMark ? -1 : static_cast<int>(up);
           }
-        } else if (!full) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int nh = nk - 32 * i;
-            mk[i] = nh >= 32 ? 0xffffffffu : (nh <= 0 ? 0u : ((1u << nh) - 1u));
-          }
         }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.s_full[half], (it >> 1) & 1, abort));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.s_full[half], phase, abort));
         fence_after();
         if (live && ok) {
-          // Two forms of one computation: a full prefix tile holds its 128
-          // scores in registers; the others (one or two per piece) mask them,
-          // 32 at a time in loops that are not unrolled, and read them twice:
-          // code that runs once per piece is fetched each time, and fetching
-          // it costs more than running it.
-          float nmu, factor = 1.f;
-          bool grow;
-          auto take = [&](const float* mx) {              // the tile's maximum into the row's state
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-            const float m_new = fmaxf(m_run, mt);
-            grow = m_new > m_run + 8.0f;                  // also the first finite maximum
-            if (grow) {
-              factor = ex2_approx(m_run - m_new);         // 0 when m_run = -inf
-              m_run = m_new;
-            }
-            nmu = (m_run == -INFINITY) ? 0.f : -m_run;
-          };
-          // p = 2^(s sl2 - m) as bf16 pairs over the first half of S, behind
-          // the columns already read
-          float ps[4] = {0.f, 0.f, 0.f, 0.f};
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          if (full) {
-            float s[128];
+          float s[128];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32(scol + q * 32, s + q * 32);
-            tmem_wait_ld();
+          for (int q = 0; q < 4; ++q) tmem_ld32(scol + q * 32, s + q * 32);
+          tmem_wait_ld();
+          if (!full) {
 #pragma unroll
-            for (int k = 0; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
-            take(mx);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                const float a = ex2_approx(fmaf(s[q * 32 + k], sl2, nmu));
-                const float b = ex2_approx(fmaf(s[q * 32 + k + 1], sl2, nmu));
-                ps[k & 2] += a;
-                ps[(k & 2) + 1] += b;
-                pk[k / 2] = pack_bf16(a, b);
-              }
-              tmem_st16u(scol + q * 16, pk);
-            }
-          } else {
-            auto mask = [&](int q) { return q == 0 ? mk[0] : (q == 1 ? mk[1] : (q == 2 ? mk[2] : mk[3])); };
-            float s[32];
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              tmem_ld32(scol + q * 32, s);
-              tmem_wait_ld();
-              const uint32_t m = mask(q);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], ((m >> k) & 1u) ? s[k] : -INFINITY);
-            }
-            take(mx);
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              tmem_ld32(scol + q * 32, s);
-              tmem_wait_ld();
-              const uint32_t m = mask(q);
-              uint32_t pk[16];
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                const float a = ((m >> k) & 1u) ? ex2_approx(fmaf(s[k], sl2, nmu)) : 0.f;
-                const float b = ((m >> (k + 1)) & 1u) ? ex2_approx(fmaf(s[k + 1], sl2, nmu)) : 0.f;
-                ps[k & 2] += a;
-                ps[(k & 2) + 1] += b;
-                pk[k / 2] = pack_bf16(a, b);
-              }
-              tmem_st16u(scol + q * 16, pk);
-              tmem_wait_st();
-            }
+            for (int x = 0; x < 128; ++x) s[x] = ((mk[x >> 5] >> (x & 31)) & 1u) ? s[x] : -INFINITY;
           }
-          l_run = l_run * factor + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
-          if (__any_sync(0xffffffffu, grow) && r >= 2) {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int x = 0; x < 128; x += 2) mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], s[x], s[x + 1]);
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+          const float m_new = fmaxf(m_run, mt);
+          const bool grow = m_new > m_run + 8.0f;         // also the first finite maximum
+          float factor = 1.f;
+          if (grow) {
+            factor = ex2_approx(m_run - m_new);           // 0 when m_run = -inf
+            m_run = m_new;
+          }
+          const float nmu = (m_run == -INFINITY) ? 0.f : -m_run;
+          // p = 2^(s sl2 - m) as bf16 pairs over the first half of S
+          float2 ps[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+          const float2 sl = make_float2(sl2, sl2), nm = make_float2(nmu, nmu);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              float2 e = fma2(make_float2(s[q * 32 + x], s[q * 32 + x + 1]), sl, nm);
+              e.x = ex2_approx(e.x);
+              e.y = ex2_approx(e.y);
+              ps[(x >> 1) & 3] = add2(ps[(x >> 1) & 3], e);
+              pk[x / 2] = pack_bf16(e.x, e.y);
+            }
+            tmem_st16u(scol + q * 16, pk);
+          }
+          const float2 sum = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
+          l_run = l_run * factor + (sum.x + sum.y);
+          if (__any_sync(0xffffffffu, grow) && r > r0) {
             // O_h holds the group's tiles before this one (their P V is done:
             // this tile's S was issued behind it): rescale
-            fence_after();
 #pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
               float o[16];
@@ -646,111 +679,125 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           }
           tmem_wait_st();
         }
-        if (!full) {
-          // V rows that are no keys are cleared; a tree tile's rows are looked over
+        if (!full && (!PAIR || half == 0)) {
+          // V rows of the K steps that are no keys are cleared, nodes' rows looked over
           ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.v_full[it % VS], (it / VS) & 1, abort));
-          uint8_t* v0 = gbase + Sh::kV + (it % VS) * TB + row * 128;
-          uint32_t* vbad = bars.vbad[half][(it >> 1) & 1];
-          bool hit = false;
-          if (ok && (row >= nk || tree)) {
-#pragma unroll 4
-            for (int ch = 0; ch < D / 8; ++ch) {
-              uint4* at = reinterpret_cast<uint4*>(v0 + (ch >> 3) * kHalfBytes + (((ch & 7) ^ (row & 7)) << 4));
-              if (row >= nk) {
-                *at = make_uint4(0u, 0u, 0u, 0u);
-              } else {
-                uint4 x = *at;
-                uint32_t e[4] = {x.x, x.y, x.z, x.w};
+          uint8_t* v0 = gbase + Sh::kV + (it % VS) * TB;
+          uint32_t* vbad = bars.vbad[half][nfix & 3];
+          auto chunk = [&](int x, int ch) {
+            return reinterpret_cast<uint4*>(v0 + x * 128 + (ch >> 3) * kHalfBytes + (((ch & 7) ^ (x & 7)) << 4));
+          };
+          constexpr int CPR = D / 8;
+          if (ok) {
+            const int top = (end + 15) & ~15;
+            for (int e = tid & 127; e < (top - np) * CPR; e += 128) {
+              const int x = np + e / CPR;
+              if (!tree || x < off || x >= end) *chunk(x, e % CPR) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (tree) {
+              for (int e = tid & 127; e < (end - off) * CPR; e += 128) {
+                const int x = off + e / CPR;
+                uint4* at = chunk(x, e % CPR);
+                const uint4 v = *at;
+                uint32_t u[4] = {v.x, v.y, v.z, v.w};
                 bool h = false;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  if ((e[i] & 0x7f80u) == 0x7f80u) { e[i] &= 0xffff0000u; h = true; }
-                  if ((e[i] & 0x7f800000u) == 0x7f800000u) { e[i] &= 0xffffu; h = true; }
+                  if ((u[i] & 0x7f80u) == 0x7f80u) { u[i] &= 0xffff0000u; h = true; }
+                  if ((u[i] & 0x7f800000u) == 0x7f800000u) { u[i] &= 0xffffu; h = true; }
                 }
-                if (h) { *at = make_uint4(e[0], e[1], e[2], e[3]); hit = true; }
+                if (h) {
+                  *at = make_uint4(u[0], u[1], u[2], u[3]);
+                  atomicOr(vbad + (x >> 5), 1u << (x & 31));
+                }
               }
             }
           }
-          if (hit) atomicOr(vbad + (row >> 5), 1u << (row & 31));
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (tree) {
-            // every warp of the group comes here for every tree tile, after an abort too
-            bar_sync(2 + half, 128);
-            uint32_t any = 0, seen = 0;
+          // every warp of the group comes here for every tree tile, after an abort too
+          if (tree) bar_sync(2 + half, 128);
+          if (PAIR && tree && lane == 0) mbar_arrive(&bars.vfix);
+        }
+        if (tree) {
+          if (PAIR && half == 1) ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.vfix, nfix & 1, abort));
+          const volatile uint32_t* vbad = bars.vbad[PAIR ? 0 : half][nfix & 3];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t x = *reinterpret_cast<volatile uint32_t*>(vbad + i);
-              any |= x;
-              seen |= x & mk[i];
-            }
-            if (any) {
-              nf = nf || seen;
-              bar_sync(2 + half, 128);
-              if ((tid & 127) < 4) vbad[tid & 3] = 0;
-              bar_sync(2 + half, 128);
-            }
-          }
+          for (int i = 0; i < 4; ++i) nf = nf || (vbad[i] & mk[i]);
+          // the slot after next was last read two tree tiles ago
+          if ((!PAIR || half == 0) && (tid & 127) < 4) bars.vbad[half][(nfix + 2) & 3][tid & 3] = 0;
+          ++nfix;
         }
         fence_before();
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(&bars.p_full[half]);
       }
       // ---------------------------------------------------------- output
-      // the group's last P V; tiles two apart complete in order, so one phase is enough
+      const int g0 = it0 & 1;                             // (one row tile) the group of the piece's first tile
       it0 += cnt;
       if (cnt > r0) {
-        const int last = it0 - 1 - ((it0 - 1 - half) & 1);
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.pv_done[half], (last >> 1) & 1, abort));
+        // the group's last P V
+        const int last = PAIR ? it0 - 1 : (it0 - 1 - ((it0 - 1 - half) & 1)) >> 1;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.pv_done[half], static_cast<uint32_t>(last) & 1u, abort));
       }
-      // the groups meet: M = max(m_0, m_1), c_h = 2^(m_h - M),
-      // O = (c_0 O_0 + c_1 O_1) / (c_0 l_0 + c_1 l_1); group h writes d columns DH h ..
-      bars.red_m[half][row] = m_run;
-      bars.red_l[half][row] = l_run;
-      bars.red_nf[half][row] = nf + 2 * !my_ok;
-      fence_before();
-      bar_sync(1, kSoftmaxThreads);
       fence_after();
-      const float m_0 = bars.red_m[0][row], m_1 = bars.red_m[1][row];
-      const float l_0 = bars.red_l[0][row], l_1 = bars.red_l[1][row];
-      nf = ((bars.red_nf[0][row] | bars.red_nf[1][row]) & 1) != 0;
-      my_ok = ((bars.red_nf[0][row] | bars.red_nf[1][row]) & 2) == 0;
-      const float M = fmaxf(m_0, m_1);
-      const float c_0 = (m_0 == -INFINITY) ? 0.f : ex2_approx(m_0 - M);
-      const float c_1 = (m_1 == -INFINITY) ? 0.f : ex2_approx(m_1 - M);
-      // a group whose sum is NaN (a NaN score) makes the row NaN
-      const float l_row = c_0 * l_0 + c_1 * l_1 + ((l_0 != l_0 || l_1 != l_1) ? NAN : 0.f);
-      const bool have_0 = cnt > (it0 - cnt & 1 ? 1 : 0), have_1 = cnt > (it0 - cnt & 1 ? 0 : 1);   // tiles of group 0, 1
-      const bool bad = c.s.bad_len || !my_ok || !ok || bars.bad_piece[w.index & 7] == w.index + 1;
+      float c_0, c_1, M, l_row;                           // weights of O_0, O_1; maximum and sum
+      bool have_0, have_1;                                // accumulators that hold something
+      if (PAIR) {
+        have_0 = cnt > 0 && half == 0;
+        have_1 = cnt > 0 && half == 1;
+        c_0 = c_1 = 1.f;
+        M = m_run;
+        l_row = l_run;
+      } else {
+        // the groups meet: M = max(m_0, m_1), c_h = 2^(m_h - M),
+        // O = (c_0 O_0 + c_1 O_1) / (c_0 l_0 + c_1 l_1); group h writes half of the columns
+        bars.red_m[half][row] = m_run;
+        bars.red_l[half][row] = l_run;
+        bars.red_nf[half][row] = nf + 2 * !my_ok;
+        fence_before();
+        bar_sync(1, kSoftmaxThreads);
+        fence_after();
+        const float m_0 = bars.red_m[0][row], m_1 = bars.red_m[1][row];
+        const float l_0 = bars.red_l[0][row], l_1 = bars.red_l[1][row];
+        nf = ((bars.red_nf[0][row] | bars.red_nf[1][row]) & 1) != 0;
+        my_ok = ((bars.red_nf[0][row] | bars.red_nf[1][row]) & 2) == 0;
+        M = fmaxf(m_0, m_1);
+        c_0 = (m_0 == -INFINITY) ? 0.f : ex2_approx(m_0 - M);
+        c_1 = (m_1 == -INFINITY) ? 0.f : ex2_approx(m_1 - M);
+        // a group whose sum is NaN (a NaN score) makes the row NaN
+        l_row = c_0 * l_0 + c_1 * l_1 + ((l_0 != l_0 || l_1 != l_1) ? NAN : 0.f);
+        have_0 = cnt > g0;
+        have_1 = cnt > 1 - g0;
+      }
+      const bool bad = d->bad_len || !my_ok || !ok || bars.bad_piece[d->index & 7] == d->index + 1;
       const bool empty = l_row == 0.f;
       const float inv = bad ? NAN : (empty ? 0.f : 1.f / l_row);
       const float w_0 = c_0 * inv, w_1 = c_1 * inv;
-      const bool whole = c.t0 == 0 && c.t1 == c.s.len;
-      const int packed = w.i0 * G + row;
-      const int which = c.t0 == 0 ? 1 : 0;
-      const int64_t slot = part_slot(p, blockIdx.x, which, kRows) + row;
+      const bool whole = d->whole;
+      const int packed = (d->i0 + first) * G + row;
+      const int64_t slot = part_slot(p, blockIdx.x, d->begins ? 1 : 0) + first * G + row;
       if (live) {
-        __nv_bfloat16* orow = row_valid ? out_row<__nv_bfloat16>(p, c.b, c.g, packed) : nullptr;
+        __nv_bfloat16* orow = row_valid ? out_row<__nv_bfloat16>(p, d->b, d->g, packed) : nullptr;
+        constexpr int NC = PAIR ? D : D / 2;              // columns of a thread
 #pragma unroll 1
-        for (int q = 0; q < DH / 16; ++q) {
-          const int col = half * DH + q * 16;
-          float v0[16], v1[16];
-          if (have_0) tmem_ld16(trow + kColO + col, v0);
-          if (have_1) tmem_ld16(trow + kColO + 128 + col, v1);
+        for (int q = 0; q < NC / 32; ++q) {
+          const int col = (PAIR ? 0 : half * NC) + q * 32;
+          float v0[32], v1[32];
+          if (have_0) tmem_ld32(trow + kColO + col, v0);
+          if (have_1) tmem_ld32(trow + kColO + 128 + col, v1);
           tmem_wait_ld();
           if (!row_valid) continue;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            // an accumulator that no tile wrote is not looked at
+          for (int e = 0; e < 32; ++e)
             v0[e] = (have_0 ? w_0 * v0[e] : 0.f) + (have_1 ? w_1 * v1[e] : 0.f) + (bad ? NAN : 0.f);
-          }
           if (nf) {
             // the values that are not finite, of the nodes this row sees
             int j = my_node;
             while (true) {
-              const __nv_bfloat16* vs = static_cast<const __nv_bfloat16*>(p.vt) + c.b * p.kt_sb +
-                                        static_cast<int64_t>(j) * p.kt_st + static_cast<int64_t>(c.g) * p.kt_sh + col;
+              const __nv_bfloat16* vs = static_cast<const __nv_bfloat16*>(p.vt) + d->b * p.kt_sb +
+                                        static_cast<int64_t>(j) * p.kt_st + static_cast<int64_t>(d->g) * p.kt_sh + col;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
+              for (int e = 0; e < 32; ++e) {
                 const float x = __bfloat162float(vs[e]);
                 if (!(fabsf(x) < INFINITY)) v0[e] += x;
               }
@@ -761,7 +808,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           }
           if (whole) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 4; ++e) {
               uint4 x;
               x.x = pack_bf16(v0[8 * e], v0[8 * e + 1]);
               x.y = pack_bf16(v0[8 * e + 2], v0[8 * e + 3]);
@@ -771,33 +818,41 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 8; ++e)
               *reinterpret_cast<float4*>(p.part_o + slot * D + col + 4 * e) =
                   make_float4(v0[4 * e], v0[4 * e + 1], v0[4 * e + 2], v0[4 * e + 3]);
           }
         }
-        if (half == 0 && row_valid) {
+        if ((PAIR || half == 0) && row_valid) {
           const float lse2 = bad ? NAN : (empty ? -INFINITY : M + log2f(l_row));
           if (!whole) p.part_lse[slot] = lse2;
-          else if (p.lse) p.lse[lse_row(p, c.b, c.g, packed)] = lse2 * kLn2;
+          else if (p.lse) p.lse[lse_row(p, d->b, d->g, packed)] = lse2 * kLn2;
           if (!my_ok) set_status(p.status, TV_DEV_BAD_PARENT);
         }
       }
-      // the accumulators are free for the next piece
+      // the accumulators and parent[] are free for the pieces to come
       fence_before();
       __syncwarp();
-      if (lane == 0 && cnt > 0) mbar_arrive(&bars.o_free);
-      if (tid == 0) {
-        if (bars.bad_piece[w.index & 7] == w.index + 1) set_status(p.status, TV_DEV_BAD_PAGE);
-        if (!ok) set_status(p.status, TV_DEV_TIMEOUT);
+      if (lane == 0 && cnt > 0) {
+        if (PAIR) {
+          mbar_arrive(&bars.o_free[half]);
+        } else {
+          mbar_arrive(&bars.o_free[0]);
+          mbar_arrive(&bars.o_free[1]);
+        }
       }
-      if (w.t.b1 > w.t.b0) {
-        __syncwarp();
+      if (d->ntr > 0) {
         if (lane == 0) mbar_arrive(&bars.t_empty[ntree & 1]);
         ++ntree;
       }
-      if (tid == 0 && c.t0 == 0 && !whole) split = split_of(ln, c, w.i0 * G, rows_here);
-      bar_sync(1, kSoftmaxThreads);                       // red_*: read by all
+      if (tid == 0) {
+        if (bars.bad_piece[d->index & 7] == d->index + 1) set_status(p.status, TV_DEV_BAD_PAGE);
+        if (!ok) set_status(p.status, TV_DEV_TIMEOUT);
+        if (d->begins && !whole) split = SplitUnit{d->c1, d->b, d->g, d->i0 * G, d->nodes * G};
+      }
+      if (!PAIR) bar_sync(1, kSoftmaxThreads);            // red_*: read by all
+      __syncwarp();
+      if (lane == 0) release(k);
     }
     if (tid == 0) p.splits[blockIdx.x] = split;
   }
@@ -817,23 +872,29 @@ int64_t stride_or(int64_t dim, int64_t s) { return dim > 1 ? s : 128; }
 
 bool stride_ok(int64_t dim, int64_t s) { return dim <= 1 || (s > 0 && s % 8 == 0 && s * 2 < (1ll << 40)); }
 
-int page_box(int P) {
+template <int D, bool PAIR>
+cudaError_t launch(const PagedAttnParams& p, int grid, const CUtensorMap* m, cudaStream_t stream) {
+  constexpr size_t smem = Shape<D, PAIR>::kBytes + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(attn_paged_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  attn_paged_tc_kernel<D, PAIR><<<grid, kThreads, smem, stream>>>(m[0], m[1], m[2], m[3], m[4], p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int attn_paged_tc_box(int P) {
   int b = 128;
   while (b >= 8 && P % b != 0) b /= 2;
   return b >= 8 ? b : 0;
 }
 
-template <int D>
-cudaError_t launch(const PagedAttnParams& p, int grid, int box, const CUtensorMap* m, cudaStream_t stream) {
-  constexpr size_t smem = Shape<D>::kBytes + 1024;
-  const cudaError_t e = cudaFuncSetAttribute(attn_paged_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  attn_paged_tc_kernel<D><<<grid, kThreads, smem, stream>>>(m[0], m[1], m[2], m[3], m[4], p, box);
-  return cudaGetLastError();
+// One row tile, or two where a sequence can have more rows than one holds.
+int attn_paged_tc_rows(const tv_attn_paged_args* a) {
+  const int G = a->Hq / a->Hkv, tile = kRows / G * G;
+  return static_cast<int64_t>(a->T) * G > tile ? 2 * tile : tile;
 }
-
-}  // namespace
 
 bool attn_paged_tc_supported(const tv_attn_paged_args* a) {
   if (a->dtype != TV_BF16 || (a->d != 64 && a->d != 128)) return false;
@@ -850,24 +911,26 @@ bool attn_paged_tc_supported(const tv_attn_paged_args* a) {
 
 cudaError_t launch_attn_paged_tc(const PagedAttnParams& p, int grid, cudaStream_t stream) {
   CUtensorMap m[5];
-  const int box = page_box(p.page_size);
+  const int tile = kRows / p.G * p.G;
   auto map = [&](CUtensorMap* t, const void* x, int64_t d1, int64_t d2, int64_t d3, int64_t s1, int64_t s2, int64_t s3,
                  int b1, int b2) {
     return tcmap::make_map(t, x, p.d, d1, d2, d3, stride_or(d1, s1), stride_or(d2, s2), stride_or(d3, s3), b1, b2);
   };
-  if (!map(&m[0], p.q, p.Hq, p.T, p.B, p.q_sh, p.q_st, p.q_sb, p.G, p.rows / p.G) ||
-      !map(&m[3], p.kt, p.Hkv, p.T, p.B, p.kt_sh, p.kt_st, p.kt_sb, 1, kKeys) ||
-      !map(&m[4], p.vt, p.Hkv, p.T, p.B, p.kt_sh, p.kt_st, p.kt_sb, 1, kKeys))
+  if (!map(&m[0], p.q, p.Hq, p.T, p.B, p.q_sh, p.q_st, p.q_sb, p.G, tile / p.G) ||
+      !map(&m[3], p.kt, p.Hkv, p.T, p.B, p.kt_sh, p.kt_st, p.kt_sb, 1, kTreeBox) ||
+      !map(&m[4], p.vt, p.Hkv, p.T, p.B, p.kt_sh, p.kt_st, p.kt_sb, 1, kTreeBox))
     return cudaErrorInvalidValue;
-  if (box > 0) {
-    if (!map(&m[1], p.kp, p.Hkv, p.page_size, p.num_pages, p.kv_sh, p.kv_sr, p.kv_sp, 1, box) ||
-        !map(&m[2], p.vp, p.Hkv, p.page_size, p.num_pages, p.kv_sh, p.kv_sr, p.kv_sp, 1, box))
+  if (p.box > 0) {
+    if (!map(&m[1], p.kp, p.Hkv, p.page_size, p.num_pages, p.kv_sh, p.kv_sr, p.kv_sp, 1, p.box) ||
+        !map(&m[2], p.vp, p.Hkv, p.page_size, p.num_pages, p.kv_sh, p.kv_sr, p.kv_sp, 1, p.box))
       return cudaErrorInvalidValue;
   } else {
     m[1] = m[3];
     m[2] = m[4];
   }
-  return p.d == 64 ? launch<64>(p, grid, box, m, stream) : launch<128>(p, grid, box, m, stream);
+  const bool pair = p.rows > tile;
+  if (p.d == 64) return pair ? launch<64, true>(p, grid, m, stream) : launch<64, false>(p, grid, m, stream);
+  return pair ? launch<128, true>(p, grid, m, stream) : launch<128, false>(p, grid, m, stream);
 }
 
 }  // namespace tv

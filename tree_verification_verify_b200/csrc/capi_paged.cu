@@ -83,7 +83,7 @@ PagedPlan plan_attn_paged(const tv_attn_paged_args* a) {
   PagedPlan pl;
   const int G = a->Hq / a->Hkv;
   pl.tc = attn_paged_tc_supported(a);
-  pl.rows = pl.tc ? 128 / G * G : attn_paged_simt_rows(static_cast<int64_t>(a->T) * G);
+  pl.rows = pl.tc ? attn_paged_tc_rows(a) : attn_paged_simt_rows(static_cast<int64_t>(a->T) * G);
   const int keys = pl.tc ? 128 : 64;
   // no more CTAs than key tiles can be
   const int64_t rt = (static_cast<int64_t>(a->T) * G + pl.rows - 1) / pl.rows;
@@ -92,8 +92,7 @@ PagedPlan plan_attn_paged(const tv_attn_paged_args* a) {
   pl.fits = most < (1ll << 31);
   const int64_t want = static_cast<int64_t>(num_sms()) * (pl.tc ? 1 : attn_paged_simt_ctas(pl.rows, a->d));
   pl.grid = static_cast<int>(most < want ? (most > 0 ? most : 1) : want);
-  const size_t tile_rows = pl.tc ? 128 : pl.rows;
-  const size_t slots = static_cast<size_t>(pl.grid) * 2 * tile_rows;
+  const size_t slots = static_cast<size_t>(pl.grid) * 2 * pl.rows;
   size_t off = kTicketBytes;
   pl.off_o = off;   off = align256(off + slots * a->d * sizeof(float));
   pl.off_lse = off; off = align256(off + slots * sizeof(float));
@@ -142,6 +141,7 @@ extern "C" tv_status tree_verify_attn_paged(const tv_attn_paged_args* a, void* w
   p.status = a->dev_status;
   p.prefix_only = a->prefix_only;
   p.rows = pl.rows;
+  p.box = pl.tc ? attn_paged_tc_box(a->page_size) : 0;
   unsigned char* w = static_cast<unsigned char*>(ws);
   p.splits = reinterpret_cast<SplitUnit*>(w + pl.off_splits);
   p.part_o = reinterpret_cast<float*>(w + pl.off_o);
@@ -149,7 +149,7 @@ extern "C" tv_status tree_verify_attn_paged(const tv_attn_paged_args* a, void* w
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = pl.tc ? launch_attn_paged_tc(p, pl.grid, s) : launch_attn_paged_simt(p, pl.grid, s);
   if (e != cudaSuccess) return TV_ERR_CUDA;
-  return from_cuda(launch_attn_paged_merge(p, pl.grid, pl.tc ? 128 : pl.rows, s));
+  return from_cuda(launch_attn_paged_merge(p, pl.grid, s));
 }
 
 // ------------------------------------------------------------ acceptance
