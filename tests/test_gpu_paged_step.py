@@ -510,8 +510,10 @@ def test_a_server_over_pages_equals_contiguous_caches():
         graph.replay()
         torch.cuda.synchronize()
         out, lse, o, n_free = outs
-        # both sides round weights and outputs to bf16 (values near 1): 2 (2^-8 + 2^-8)
-        assert (out.float() - ref.float()).abs().max() < 2.0 ** -6 and (lse - rlse).abs().max() < 1e-4
+        # each side rounds its weights (2^-8 of sum p |v|) and its output (2^-8 of |o|) to bf16, and both sums are at
+        # most the largest |v|, which passes 4 here: 4 * 2^-8 of it in all (1/64 alone is one step of a value in [2, 4))
+        vmax = max(flat[1].abs().max().item(), io["vt"].abs().max().item())
+        assert (out.float() - ref.float()).abs().max() <= 2.0 ** -6 * vmax and (lse - rlse).abs().max() < 1e-4
         np.testing.assert_array_equal(o["out_tokens"].cpu().numpy(), want["out_tokens"])
         tv.tree_commit_kv(flat[0], flat[1], flen, io["kt"][0], io["vt"][0], o["n_accepted"], o["accepted_nodes"])
         assert torch.equal(lens, flen) and int(st.item()) == 0

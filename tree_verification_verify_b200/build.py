@@ -1,4 +1,5 @@
-"""Build libtreeverify.so in-tree with nvcc for sm_100a.
+"""Build libtreeverify.so (nvcc, sm_100a) and _paged.so, the binding of the
+paged calls (g++, against the installed torch), in-tree.
 
     python -m tree_verification_verify_b200.build
 """
@@ -7,8 +8,10 @@ from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -22,31 +25,60 @@ NVCC_FLAGS = [
 ]
 
 
+BINDING = os.path.join(HERE, "_paged.so")
+BINDING_SRC = os.path.join(CSRC, "paged_binding.cpp")
+
+
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def _older(out: str, deps) -> bool:
+    if not os.path.exists(out):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(ROOT, "include", "*.h"))
+    t = os.path.getmtime(out)
     return any(os.path.getmtime(f) > t for f in deps)
 
 
+def _headers():
+    return glob.glob(os.path.join(ROOT, "include", "*.h"))
+
+
+def _stale() -> bool:
+    return _older(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + _headers())
+
+
+def binding_command(out: str):
+    """g++ command of the binding."""
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(shutil.which(os.environ.get("NVCC", "nvcc")) or "/usr/local/cuda/bin/nvcc"))
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [f"-I{i}" for i in inc] + \
+        [BINDING_SRC, "-o", out, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+         "-lc10_cuda", "-L" + os.path.join(cuda, "lib64"), "-lcudart"]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA source into one shared library (skipped when up to
-    date).  Returns the library path."""
-    if not force and not _stale():
-        return LIB
+    """Compile the CUDA sources into one shared library, and the binding
+    (each skipped when up to date).  Returns the library path."""
     nvcc = os.environ.get("NVCC", "nvcc")
-    tmp = LIB + ".tmp"
-    cmd = [nvcc] + NVCC_FLAGS + ["-I", os.path.join(ROOT, "include")] + sources() + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    jobs = []
+    if force or _stale():
+        jobs.append((LIB, [nvcc] + NVCC_FLAGS + ["-I", os.path.join(ROOT, "include")] + sources() + ["-o", LIB + ".tmp"]))
+    if force or _older(BINDING, [BINDING_SRC] + _headers()):
+        jobs.append((BINDING, binding_command(BINDING + ".tmp")))
+    procs = []
+    for _, cmd in jobs:
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        procs.append(subprocess.Popen(cmd))
+    for (out, cmd), p in zip(jobs, procs):
+        if p.wait() != 0:
+            raise subprocess.CalledProcessError(p.returncode, cmd)
+        os.replace(out + ".tmp", out)
     return LIB
 
 
