@@ -2,14 +2,22 @@
 // tree_pages_compact.
 //
 // All three move rows of K and V between places that tables on the device
-// name.  Update and compaction run as two kernels.  The first, one cluster
-// of eight CTAs, marks the pages in use in a bitmap, ranks the free pages by
-// a prefix sum over its words and gives every sequence its place in that
-// list; its steps are separated by cluster barriers, so it needs neither a
-// cleared workspace nor a grid-wide wait.  The second writes the new tables
-// and copies the rows over the whole GPU.  Results depend on ranks alone,
-// never on the order in which threads arrive.
+// name.  Update and compaction first need a plan of the whole pool: the pages
+// in use as a bitmap, the free ones ranked by a prefix sum over its words,
+// every sequence's place in that order.
+//   Small pools (16384 table entries, 32768 pages, 256 sequences at most)
+//   run as one kernel: every CTA makes the plan for itself in shared memory,
+//   a few us of three dependent reads, and does its part of the copies.
+//   (With the plan in a kernel of its own 4 beams took 20.6 us, most of it
+//   two launches and five cluster barriers.)
+//   Larger ones run as two: one cluster of eight CTAs makes the plan, its
+//   steps separated by cluster barriers, so it needs neither a cleared
+//   workspace nor a grid-wide wait; the second kernel writes the new tables
+//   and copies the rows over the whole GPU.
+// Results depend on ranks alone, never on the order in which threads arrive.
 #include <cooperative_groups.h>
+
+#include <algorithm>
 #include <initializer_list>
 
 #include "tv_common.cuh"
@@ -23,6 +31,10 @@ namespace pages {
 constexpr int kThreads = 256;
 constexpr int kPlanThreads = 1024;               // of one CTA of the plan
 constexpr int kPlanCtas = 8;                     // a portable cluster
+constexpr int kSmallThreads = 512;               // of a CTA that plans for itself
+constexpr int kSmallSlice = 4 * kSmallThreads;   // words of a page of a layer that a CTA copies at a time
+constexpr int64_t kSmallEntries = 16384;
+constexpr int kSmallPages = 32768, kSmallSeqs = 256;
 constexpr int kTicketBytes = 64 * 1024;
 
 // Rows of one tensor: element strides of a (row, head) vector, and whether
@@ -35,6 +47,10 @@ struct Pool {
   int dense;                   // a page's rows are one run of bytes
 };
 
+__host__ __device__ inline int small_slices(int P, int words_per_row) {
+  return static_cast<int>((static_cast<int64_t>(P) * words_per_row + kSmallSlice - 1) / kSmallSlice);
+}
+
 template <typename W>
 __device__ __forceinline__ W ldw(const char* p) { return *reinterpret_cast<const W*>(p); }
 template <typename W>
@@ -42,17 +58,17 @@ __device__ __forceinline__ void stw(char* p, W v) { *reinterpret_cast<W*>(p) = v
 
 // Copies words [w0, w1) of `rows` rows from page address s to page address d
 // (byte offsets into k and v), by the calling CTA.
-template <typename W>
+template <typename W, int NT>
 __device__ __forceinline__ void copy_words(const Pool& pl, int64_t d, int64_t s, int w0, int w1) {
   const int wpv = pl.vec_bytes / static_cast<int>(sizeof(W));
   const int wpr = wpv * pl.Hkv;
   constexpr int U = 4;
-  for (int i0 = w0 + threadIdx.x; i0 < w1; i0 += U * kThreads) {
+  for (int i0 = w0 + threadIdx.x; i0 < w1; i0 += U * NT) {
     W a[U], b[U];
     int64_t off[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kThreads;
+      const int i = i0 + u * NT;
       if (i < w1) {
         if (pl.dense) {
           off[u] = static_cast<int64_t>(i) * sizeof(W);
@@ -66,7 +82,7 @@ __device__ __forceinline__ void copy_words(const Pool& pl, int64_t d, int64_t s,
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i0 + u * kThreads < w1) {
+      if (i0 + u * NT < w1) {
         stw<W>(pl.k + d + off[u], a[u]);
         stw<W>(pl.v + d + off[u], b[u]);
       }
@@ -74,9 +90,10 @@ __device__ __forceinline__ void copy_words(const Pool& pl, int64_t d, int64_t s,
   }
 }
 
-// Exclusive prefix sum of v over a CTA of the plan; *total is the sum.
+// Exclusive prefix sum of v over a CTA of NT threads; *total is the sum.
+template <int NT = kPlanThreads>
 __device__ __forceinline__ int block_scan(int v, int* total) {
-  __shared__ int ws[kPlanThreads / 32];
+  __shared__ int ws[NT / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = v;
 #pragma unroll
@@ -89,12 +106,68 @@ __device__ __forceinline__ int block_scan(int v, int* total) {
   __syncthreads();
   int before = 0, sum = 0;
 #pragma unroll
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
+  for (int w = 0; w < NT / 32; ++w) {
     before += w < warp ? ws[w] : 0;
     sum += ws[w];
   }
   *total = sum;
   return before + incl - v;
+}
+
+// Exclusive prefix sums of n shared-memory counts in place; returns the sum.
+template <int NT>
+__device__ __forceinline__ int scan_array(int* v, int n) {
+  int base = 0;
+  for (int i0 = 0; i0 < n; i0 += NT) {
+    const int i = i0 + static_cast<int>(threadIdx.x);
+    const int x = i < n ? v[i] : 0;
+    int sum;
+    const int before = block_scan<NT>(x, &sum);
+    if (i < n) v[i] = base + before;
+    base += sum;
+  }
+  __syncthreads();
+  return base;
+}
+
+// f(b, i, entry i of row(b)) for the first held(b) entries of every sequence: a
+// warp per sequence, four sequences' loads in flight.
+template <int NT, typename Held, typename Row, typename F>
+__device__ __forceinline__ void for_entries(int B, Held held, Row row, F f) {
+  constexpr int kWarps = NT / 32, U = 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int b0 = warp; b0 < B; b0 += U * kWarps) {
+    int h[U], most = 0;
+    const int32_t* r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + u * kWarps;
+      h[u] = b < B ? held(b) : 0;
+      r[u] = b < B ? row(b) : nullptr;
+      most = max(most, h[u]);
+    }
+    for (int i = lane; i < most; i += 32) {
+      int page[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) page[u] = i < h[u] ? __ldg(r[u] + i) : 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i < h[u]) f(b0 + u * kWarps, i, page[u]);
+    }
+  }
+}
+
+// Index of set bit number k of a bitmap whose words' prefix counts are known.
+template <typename F>
+__device__ __forceinline__ int select_bit(const int* before, int words, int k, F word) {
+  int lo = 0, hi = words;                        // last word with before <= k
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (before[mid] <= k) lo = mid; else hi = mid;
+  }
+  uint32_t m = word(lo);
+  for (int r = k - before[lo]; r > 0; --r) m &= m - 1u;
+  return lo * 32 + __ffs(m) - 1;
 }
 
 // The CTAs' shares of a sum: every CTA posts `mine`, and after a cluster
@@ -250,13 +323,19 @@ __device__ __forceinline__ void turn_pages(const UpdateParams& p, Turn& t) {
   t.partial = t.keep % p.P != 0 && t.grow > 0;
 }
 
-// A warp's check of sequence b: the status bits of what is wrong with it.
-__device__ __forceinline__ uint32_t check_turn(const UpdateParams& p, Turn& t, const int32_t* row) {
+// The status bits of what is wrong with a sequence's numbers.
+__device__ __forceinline__ uint32_t check_rows(const UpdateParams& p, const Turn& t) {
   uint32_t bits = 0;
   if (t.s < -1 || t.s >= p.B_in) bits |= TV_DEV_BAD_ROW;
   if (t.keep < 0 || t.grow < 0 || t.keep > static_cast<int64_t>(p.W_in) * p.P ||
       static_cast<int64_t>(t.keep) + t.grow > static_cast<int64_t>(p.W) * p.P)
     bits |= TV_DEV_BAD_LEN;
+  return bits;
+}
+
+// A warp's check of sequence b, its kept pages too.
+__device__ __forceinline__ uint32_t check_turn(const UpdateParams& p, Turn& t, const int32_t* row) {
+  const uint32_t bits = check_rows(p, t);
   if (bits) return bits;
   turn_pages(p, t);
   bool bad = false;
@@ -391,8 +470,132 @@ __global__ void __launch_bounds__(kThreads) update_apply_kernel(UpdateParams p) 
   }
   if (copies && layer < p.layers) {
     const int wpr = p.pool.Hkv * p.pool.vec_bytes / static_cast<int>(sizeof(W));
-    copy_words<W>(p.pool, layer * p.pool.sl + p.list[at] * p.pool.sp, layer * p.pool.sl + row[t.held - 1] * p.pool.sp,
+    copy_words<W, kThreads>(p.pool, layer * p.pool.sl + p.list[at] * p.pool.sp, layer * p.pool.sl + row[t.held - 1] * p.pool.sp,
                   0, t.keep % p.P * wpr);
+  }
+}
+
+// The whole update in one kernel, for small pools: every CTA plans, then takes
+// its share of the new table's rows and of the copies' slices.
+template <typename W>
+__global__ void __launch_bounds__(kSmallThreads) update_small_kernel(UpdateParams p) {
+  constexpr int NT = kSmallThreads;
+  extern __shared__ uint32_t dyn[];
+  const int words = (p.num_pages + 31) / 32;
+  uint32_t* read = dyn;                          // as in UpdateParams
+  uint32_t* write = read + words;
+  int* before = reinterpret_cast<int*>(write + words);   // free pages below a word
+  __shared__ Turn s_turn[kSmallSeqs];
+  __shared__ uint32_t s_bits[kSmallSeqs];        // what is wrong with the sequence
+  __shared__ int s_page[kSmallSeqs];             // the last page, where it is partly kept; -1
+  __shared__ int s_off[kSmallSeqs];              // place of the sequence's fresh pages
+  __shared__ int s_first[kSmallSeqs], s_list[kSmallSeqs];
+  __shared__ uint8_t s_copies[kSmallSeqs];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < p.B) {
+    Turn t = turn_of(p, tid);
+    uint32_t bits = check_rows(p, t);
+    if (!bits) turn_pages(p, t);
+    s_turn[tid] = t;
+    s_bits[tid] = bits;
+  }
+  // Mark the kept pages, all entries at once.  A bad page among them shows
+  // only here; its sequence keeps nothing, so the marks are made again
+  // without it (one round where there is none).
+  int again = 0;
+  do {
+    for (int w = tid; w < words; w += NT) write[w] = 0;
+    for (int w = warp; w < words; w += NT / 32) {
+      const int page = w * 32 + lane;
+      const unsigned m = __ballot_sync(0xffffffffu, p.pinned && page < p.num_pages && p.pinned[page] != 0);
+      if (lane == 0) read[w] = m;
+    }
+    if (tid < p.B) {
+      if (s_bits[tid]) {
+        s_turn[tid].held = s_turn[tid].want = 0;
+        s_turn[tid].partial = false;
+      }
+      s_page[tid] = -1;
+    }
+    __syncthreads();
+    int bad = 0;
+    for_entries<NT>(
+        p.B, [&](int b) { return s_turn[b].held; },
+        [&](int b) { return p.table + static_cast<int64_t>(max(s_turn[b].s, 0)) * p.pt_sb; },
+        [&](int b, int i, int page) {
+          if (page < 0 || page >= p.num_pages) {
+            s_bits[b] = TV_DEV_BAD_PAGE;
+            bad = 1;
+          } else if (i == s_turn[b].held - 1 && s_turn[b].partial) {
+            atomicOr(write + (page >> 5), 1u << (page & 31));
+            s_page[b] = page;
+          } else {
+            atomicOr(read + (page >> 5), 1u << (page & 31));
+          }
+        });
+    again = __syncthreads_or(bad);
+  } while (again);
+  if (blockIdx.x == 0 && tid < p.B) set_status(p.status, s_bits[tid]);
+  // the first sequence that writes into each partly kept page: such pages
+  // are numbered by their bits' ranks, one for a sequence at most
+  for (int w = tid; w < words; w += NT) before[w] = __popc(write[w]);
+  if (tid < p.B) s_first[tid] = p.B;
+  __syncthreads();
+  scan_array<NT>(before, words);
+  int* first = nullptr;
+  bool copies = false;                           // others read on in my last page, or an earlier sequence writes in it
+  if (tid < p.B && s_page[tid] >= 0) {
+    const int w = s_page[tid] >> 5, bit = s_page[tid] & 31;
+    first = s_first + before[w] + __popc(write[w] & ((1u << bit) - 1u));
+    atomicMin(first, tid);
+    copies = (read[w] >> bit) & 1u;
+  }
+  __syncthreads();
+  if (first) copies = copies || *first != tid;
+  int demand = 0;
+  if (tid < p.B) demand = s_turn[tid].want - s_turn[tid].held + (copies ? 1 : 0);
+  int need;
+  const int off = block_scan<NT>(demand, &need);
+  int n_copies;
+  const int k = block_scan<NT>(copies ? 1 : 0, &n_copies);
+  if (tid < p.B) {
+    s_off[tid] = off;
+    s_copies[tid] = copies;
+    if (copies) s_list[k] = tid;
+  }
+  auto free_word = [&](int w) -> uint32_t {
+    uint32_t f = ~(read[w] | write[w]);
+    if (w == words - 1 && (p.num_pages & 31)) f &= (1u << (p.num_pages & 31)) - 1u;
+    return f;
+  };
+  for (int w = tid; w < words; w += NT) before[w] = __popc(free_word(w));
+  __syncthreads();
+  const int free_pages = scan_array<NT>(before, words);
+  const bool fail = need > free_pages;
+  if (blockIdx.x == 0 && tid == 0) {
+    if (fail) set_status(p.status, TV_DEV_NO_PAGES);
+    if (p.n_free) *p.n_free = free_pages - need;
+  }
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const Turn t = s_turn[b];
+    const int32_t* row = p.table + static_cast<int64_t>(max(t.s, 0)) * p.pt_sb;
+    const int fresh0 = t.held - s_copies[b];     // first position of a fresh page
+    for (int i = tid; i < p.W; i += NT) {
+      int page = -1;
+      if (!fail && i < t.want) page = i < fresh0 ? row[i] : select_bit(before, words, s_off[b] + i - fresh0, free_word);
+      p.out[b * p.po_sb + i] = page;
+    }
+  }
+  if (fail) return;
+  const int wpr = p.pool.Hkv * (p.pool.vec_bytes / static_cast<int>(sizeof(W)));         // words of a row
+  const int slices = small_slices(p.P, wpr);
+  const int64_t jobs = static_cast<int64_t>(n_copies) * p.layers * slices;
+  for (int64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
+    const int b = s_list[j / (p.layers * slices)], rest = static_cast<int>(j % (p.layers * slices));
+    const int layer = rest / slices, w0 = rest % slices * kSmallSlice;
+    copy_words<W, NT>(p.pool, layer * p.pool.sl + select_bit(before, words, s_off[b], free_word) * p.pool.sp,
+                      layer * p.pool.sl + s_page[b] * p.pool.sp, w0,
+                      min(s_turn[b].keep % p.P * wpr, w0 + kSmallSlice));
   }
 }
 
@@ -540,8 +743,87 @@ __global__ void __launch_bounds__(kThreads) compact_apply_kernel(CompactParams p
     const int m = static_cast<int>(j / (p.layers * slices));
     const int rest = static_cast<int>(j % (p.layers * slices));
     const int layer = rest / slices, w0 = rest % slices * kSliceWords;
-    copy_words<W>(p.pool, layer * p.pool.sl + p.to[m] * p.pool.sp, layer * p.pool.sl + p.from[m] * p.pool.sp, w0,
+    copy_words<W, kThreads>(p.pool, layer * p.pool.sl + p.to[m] * p.pool.sp, layer * p.pool.sl + p.from[m] * p.pool.sp, w0,
                   min(words, w0 + kSliceWords));
+  }
+}
+
+// The whole compaction in one kernel, for small pools: every CTA plans, then
+// takes its share of the table rows and of the moves' slices.
+template <typename W>
+__global__ void __launch_bounds__(kSmallThreads) compact_small_kernel(CompactParams p) {
+  constexpr int NT = kSmallThreads;
+  extern __shared__ uint32_t dyn[];
+  const int words = (p.num_pages + 31) / 32;
+  uint32_t* used = dyn;
+  uint32_t* pin = used + words;
+  int* holes = reinterpret_cast<int*>(pin + words);      // holes, moves before a word
+  int* moves = holes + words;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int w = warp; w < words; w += NT / 32) {
+    const int page = w * 32 + lane;
+    const unsigned m = __ballot_sync(0xffffffffu, p.pinned && page < p.num_pages && p.pinned[page] != 0);
+    if (lane == 0) {
+      used[w] = 0;
+      pin[w] = m;
+    }
+  }
+  __syncthreads();
+  __shared__ int s_held[kSmallSeqs];
+  if (tid < p.B) {
+    const int len = p.length[tid];
+    s_held[tid] = used_entries(p, len);
+    if (blockIdx.x == 0 && (len < 0 || len > static_cast<int64_t>(p.W) * p.P)) set_status(p.status, TV_DEV_BAD_LEN);
+  }
+  __syncthreads();
+  const int entries = p.B * p.W;
+  uint32_t bits = 0;
+  for_entries<NT>(
+      p.B, [&](int b) { return s_held[b]; }, [&](int b) { return p.table + b * p.pt_sb; },
+      [&](int, int, int page) {
+        if (page < 0 || page >= p.num_pages) bits = TV_DEV_BAD_PAGE;
+        else atomicOr(used + (page >> 5), 1u << (page & 31));
+      });
+  if (blockIdx.x == 0) set_status(p.status, bits);
+  __syncthreads();
+  int mine = 0, total;
+  for (int w = tid; w < words; w += NT) mine += __popc(used[w] | pin[w]);
+  block_scan<NT>(mine, &total);
+  auto below = [&](int w) -> uint32_t {          // bits of word w that lie below `total`
+    return w * 32 + 32 <= total ? 0xffffffffu : (w * 32 >= total ? 0u : (1u << (total - w * 32)) - 1u);
+  };
+  auto hole_word = [&](int w) -> uint32_t { return ~(used[w] | pin[w]) & below(w); };
+  auto move_word = [&](int w) -> uint32_t { return used[w] & ~pin[w] & ~below(w); };
+  for (int w = tid; w < words; w += NT) {
+    holes[w] = __popc(hole_word(w));
+    moves[w] = __popc(move_word(w));
+  }
+  __syncthreads();
+  scan_array<NT>(holes, words);
+  const int n = scan_array<NT>(moves, words);
+  if (blockIdx.x == 0 && tid == 0 && p.n_used) *p.n_used = total;
+  for (int e = blockIdx.x * NT + tid; e < entries; e += gridDim.x * NT) {
+    const int b = e / p.W, i = e - b * p.W;
+    int page = -1;
+    if (i < s_held[b]) {
+      page = p.table[b * p.pt_sb + i];
+      if (page >= total && page < p.num_pages && !((pin[page >> 5] >> (page & 31)) & 1u)) {
+        const int k = moves[page >> 5] + __popc(move_word(page >> 5) & ((1u << (page & 31)) - 1u));
+        page = select_bit(holes, words, k, hole_word);
+      }
+    }
+    p.out[b * p.po_sb + i] = page;
+  }
+  const int wpp = p.P * p.pool.Hkv * (p.pool.vec_bytes / static_cast<int>(sizeof(W)));   // words of a page of a layer
+  const int slices = (wpp + kSmallSlice - 1) / kSmallSlice;
+  const int64_t jobs = static_cast<int64_t>(n) * p.layers * slices;
+  for (int64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
+    const int m = static_cast<int>(j / (p.layers * slices));
+    const int rest = static_cast<int>(j % (p.layers * slices));
+    const int layer = rest / slices, w0 = rest % slices * kSmallSlice;
+    const int from = select_bit(moves, words, m, move_word), to = select_bit(holes, words, m, hole_word);
+    copy_words<W, NT>(p.pool, layer * p.pool.sl + to * p.pool.sp, layer * p.pool.sl + from * p.pool.sp, w0,
+                      min(wpp, w0 + kSmallSlice));
   }
 }
 
@@ -633,6 +915,14 @@ cudaError_t launch_plan(void (*kernel)(P), const P& p, cudaStream_t stream) {
 
 }  // namespace
 
+int num_sms();
+
+namespace {
+bool small_pool(int B, int64_t entries, int num_pages) {
+  return B <= kSmallSeqs && entries <= kSmallEntries && num_pages <= kSmallPages;
+}
+}  // namespace
+
 size_t commit_paged_workspace_bytes() { return kTicketBytes; }
 size_t pages_update_workspace_bytes(int B, int num_pages) {
   UpdateParams u;
@@ -679,6 +969,19 @@ cudaError_t launch_pages_update(const tv_pages_update_args* a, void* ws, cudaStr
   p.out = a->page_table_out; p.po_sb = a->po_sb;
   p.n_free = a->n_free;
   p.status = a->dev_status;
+  if (small_pool(a->B, static_cast<int64_t>(a->B) * a->max_pages_in, a->num_pages)) {
+    const int w = word_bytes({p.pool.k, p.pool.v}, {p.pool.sl, p.pool.sp, p.pool.sr, p.pool.sh, p.pool.vec_bytes});
+    const size_t smem = static_cast<size_t>((a->num_pages + 31) / 32) * 12;
+    // a CTA for every row and every slice that can be copied, two to an SM at most
+    const int64_t jobs = static_cast<int64_t>(a->B) * a->layers * small_slices(a->page_size, a->Hkv * (p.pool.vec_bytes / w));
+    const int grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(jobs, std::max(1, a->B)), 2 * num_sms()));
+    switch (w) {
+      case 16: update_small_kernel<uint4><<<grid, kSmallThreads, smem, stream>>>(p); break;
+      case 4: update_small_kernel<uint32_t><<<grid, kSmallThreads, smem, stream>>>(p); break;
+      default: update_small_kernel<uint16_t><<<grid, kSmallThreads, smem, stream>>>(p); break;
+    }
+    return cudaGetLastError();
+  }
   carve_update(static_cast<unsigned char*>(ws), a->B, a->num_pages, p);
   cudaError_t e = launch_plan(update_plan_kernel, p, stream);
   if (e != cudaSuccess || a->B == 0) return e;
@@ -692,8 +995,6 @@ cudaError_t launch_pages_update(const tv_pages_update_args* a, void* ws, cudaStr
   return cudaGetLastError();
 }
 
-int num_sms();
-
 cudaError_t launch_pages_compact(const tv_pages_compact_args* a, void* ws, cudaStream_t stream) {
   CompactParams p;
   p.pool = make_pool(a);
@@ -703,6 +1004,21 @@ cudaError_t launch_pages_compact(const tv_pages_compact_args* a, void* ws, cudaS
   p.out = a->page_table_out; p.po_sb = a->po_sb;
   p.n_used = a->n_used;
   p.status = a->dev_status;
+  // (in place the table may not change while another CTA still plans from it)
+  if (a->page_table_out != a->page_table &&
+      small_pool(a->B, static_cast<int64_t>(a->B) * a->max_pages, a->num_pages)) {
+    const size_t smem = static_cast<size_t>((a->num_pages + 31) / 32) * 16;
+    const int w = word_bytes({p.pool.k, p.pool.v}, {p.pool.sl, p.pool.sp, p.pool.sr, p.pool.sh, p.pool.vec_bytes});
+    // at most half of the pages can move
+    const int64_t most = static_cast<int64_t>(a->num_pages) / 2 * a->layers * a->page_size * a->Hkv * (p.pool.vec_bytes / w);
+    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most / (4 * kSmallThreads) + 1, 2 * num_sms())));
+    switch (w) {
+      case 16: compact_small_kernel<uint4><<<grid, kSmallThreads, smem, stream>>>(p); break;
+      case 4: compact_small_kernel<uint32_t><<<grid, kSmallThreads, smem, stream>>>(p); break;
+      default: compact_small_kernel<uint16_t><<<grid, kSmallThreads, smem, stream>>>(p); break;
+    }
+    return cudaGetLastError();
+  }
   carve_compact(static_cast<unsigned char*>(ws), a->num_pages, p);
   cudaError_t e = launch_plan(compact_plan_kernel, p, stream);
   if (e != cudaSuccess) return e;
