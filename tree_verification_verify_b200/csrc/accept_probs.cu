@@ -15,12 +15,20 @@
 // u q(x) N < (p(x) - a q(x))^+.
 //
 // A row pass: the row is cut into consecutive chunks, one per warp of the
-// cluster, in order; lanes take four elements a step, sums are fp64 (a
-// vocabulary of fp32 terms beside a threshold).  Warps' sums meet in shared
-// memory, CTAs' sums over distributed shared memory.  A sample finds its CTA
-// and warp by the prefix of those sums and scans that warp's chunk again.
-// All CTAs of a cluster hold the same state and take the same branches.
+// cluster, in order; each warp copies its chunk of p and q into shared memory
+// (cp.async, all of it in flight at once) and sums it from there, so the
+// second rejection at a node and the final sample read nothing again.  Sums
+// are fp64 (a vocabulary of fp32 terms beside a threshold).  Warps' sums meet
+// in shared memory, CTAs' sums over distributed shared memory.  A sample
+// finds its CTA and warp by the prefix of those sums and scans that warp's
+// chunk again.  All CTAs of a cluster hold the same state and take the same
+// branches.  The loops over a chunk are kept short and rolled: a walk runs
+// them a few times only, and fetching unrolled code took longer than running
+// it (a pass of 1200 elements a warp, loads and sums unrolled by 5 steps:
+// 6.6 us).
 #include <cooperative_groups.h>
+
+#include <algorithm>
 
 #include "tv_common.cuh"
 
@@ -33,7 +41,7 @@ namespace accp {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxC = 8;
-constexpr int kMaxT = 4096;
+constexpr size_t kMaxSmem = 220 * 1024;
 
 struct Params {
   int B, T, V;
@@ -49,7 +57,9 @@ struct Params {
   int32_t* out;
   uint32_t* status;
   int vec;                     // rows start on 16 bytes
+  int rows_at;                 // byte offset of the row buffers in dynamic shared memory
   int chunk;                   // elements of a warp's chunk (a multiple of 128)
+  int cap;                     // elements of it that shared memory holds at a time (a multiple of 128)
 };
 
 __device__ __forceinline__ bool prob_ok(float x) { return x >= 0.f && x < INFINITY; }
@@ -67,12 +77,15 @@ __device__ __forceinline__ double weight(float p, float q, double a) {
 // double, are exactly its value times 2^-896 (zero and subnormal values
 // included): two integer instructions.  Sums stay in that scale, where the
 // smallest double still is 2^-178 of a probability of 1.
+// Values are taken as bits with -0 made 0, so that a probability is valid
+// exactly when they are below infinity's: a pass keeps their maximum.
 constexpr double kUnscale = 0x1p896;
-__device__ __forceinline__ double scaled(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return __hiloint2double(static_cast<int>((u >> 3) & 0x0fffffffu), static_cast<int>(u << 29));   // (-0 is 0)
+constexpr uint32_t kInvalid = 0x7f800000u;
+__device__ __forceinline__ uint32_t prob_bits(float x) { return __float_as_uint(x + 0.f); }
+__device__ __forceinline__ double scaled(uint32_t u) {
+  return __hiloint2double(static_cast<int>(u >> 3), static_cast<int>(u << 29));
 }
-__device__ __forceinline__ double weight_scaled(float p, float q, double a) {
+__device__ __forceinline__ double weight_scaled(uint32_t p, uint32_t q, double a) {
   const double w = fma(-a, scaled(q), scaled(p));
   return __double2hiint(w) < 0 ? 0.0 : w;          // (-0 too)
 }
@@ -80,6 +93,17 @@ __device__ __forceinline__ double weight_scaled(float p, float q, double a) {
 }  // namespace accp
 
 using namespace accp;
+
+__device__ __forceinline__ void cp_async16(float* dst, const float* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(float* dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
 
 template <bool SAMPLED>        // SPECSAMPLE, else SPECEXEC
 __global__ void __launch_bounds__(kThreads) accept_probs_kernel(Params P) {
@@ -148,36 +172,61 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(Params P) {
   const int e0 = static_cast<int>(min(static_cast<int64_t>(V), static_cast<int64_t>(gw) * P.chunk));
   const int e1 = static_cast<int>(min(static_cast<int64_t>(V), static_cast<int64_t>(e0) + P.chunk));
   const bool vec = P.vec != 0;
+  float* buf_p = reinterpret_cast<float*>(dyn + P.rows_at) + static_cast<size_t>(warp) * P.cap;   // [warp][cap]
+  float* buf_q = buf_p + static_cast<size_t>(kWarps) * P.cap;
+  int held_p = -1, held_q = -1;                  // rows whose whole chunk is in shared memory
+  // elements [es, ee) of a row into this warp's buffer, zeros up to a whole step
+  auto copy_in = [&](const float* row, int es, int ee, float* buf) {
+    if (vec) {
+#pragma unroll 1
+      for (int e = es + lane * 4; e + 3 < ee; e += 128) cp_async16(buf + (e - es), row + e);
+    }
+#pragma unroll 1
+    for (int e = (vec ? es + ((ee - es) & ~3) : es) + lane; e < ee; e += 32) cp_async4(buf + (e - es), row + e);
+    const int pad = (ee - es + 127) & ~127;
+    for (int e = ee - es + lane; e < pad; e += 32) buf[e] = 0.f;
+  };
+  // f(es, ee) for the pieces [es, ee) of row c's chunk, each in shared memory
+  // from element 0 of the buffers on (f true ends the walk)
+  auto pieces = [&](int c, bool with_q, auto f) {
+    for (int es = e0; es < e1; es += P.cap) {
+      const int ee = min(e1, es + P.cap);
+      const bool get_p = held_p != c, get_q = with_q && held_q != c;
+      __syncwarp();
+      if (get_p) copy_in(prow0 + static_cast<int64_t>(c) * P.tp_st, es, ee, buf_p);
+      if (get_q) copy_in(qrow0 + static_cast<int64_t>(c) * P.dp_st, es, ee, buf_q);
+      if (get_p || get_q) asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      if (f(es, ee)) return;
+    }
+    const bool whole = e1 - e0 <= P.cap;
+    held_p = whole ? c : -1;
+    if (with_q) held_q = whole ? c : -1;
+  };
+  // bits of 4 elements of the buffers
+  auto four = [](const float* buf, int o) {
+    const float4 x = *reinterpret_cast<const float4*>(buf + o);
+    return make_uint4(prob_bits(x.x), prob_bits(x.y), prob_bits(x.z), prob_bits(x.w));
+  };
   // sum of the weights of row c's residual a; NaN when the row holds an
   // invalid probability.  The parts stay in s_warp / s_cta [pass & 1].
   auto row_sum = [&](int c, double a) -> double {
-    const float* pr = prow0 + static_cast<int64_t>(c) * P.tp_st;
-    const float* qr = SAMPLED && a > 0.0 ? qrow0 + static_cast<int64_t>(c) * P.dp_st : nullptr;
     double s0 = 0.0, s1 = 0.0, s2 = 0.0, s3 = 0.0;
-    bool bad = false;
-    if (qr) {
-#pragma unroll 4
-      for (int e = e0 + lane * 4; e < e1; e += 128) {
-        const float4 pv = load4(pr, e, e1, vec, 0.f), qv = load4(qr, e, e1, vec, 0.f);
-        bad |= !(prob_ok(pv.x) && prob_ok(pv.y) && prob_ok(pv.z) && prob_ok(pv.w));
-        bad |= !(prob_ok(qv.x) && prob_ok(qv.y) && prob_ok(qv.z) && prob_ok(qv.w));
+    uint32_t top = 0;
+    const bool with_q = SAMPLED && a > 0.0;
+    pieces(c, with_q, [&](int es, int ee) {
+#pragma unroll 2
+      for (int o = lane * 4; o < ee - es; o += 128) {
+        const uint4 pv = four(buf_p, o), qv = with_q ? four(buf_q, o) : make_uint4(0u, 0u, 0u, 0u);
+        top = max(max(max(top, pv.x), max(pv.y, pv.z)), max(max(pv.w, qv.x), max(max(qv.y, qv.z), qv.w)));
         s0 += weight_scaled(pv.x, qv.x, a);
         s1 += weight_scaled(pv.y, qv.y, a);
         s2 += weight_scaled(pv.z, qv.z, a);
         s3 += weight_scaled(pv.w, qv.w, a);
       }
-    } else {
-#pragma unroll 4
-      for (int e = e0 + lane * 4; e < e1; e += 128) {
-        const float4 pv = load4(pr, e, e1, vec, 0.f);
-        bad |= !(prob_ok(pv.x) && prob_ok(pv.y) && prob_ok(pv.z) && prob_ok(pv.w));
-        s0 += scaled(pv.x);
-        s1 += scaled(pv.y);
-        s2 += scaled(pv.z);
-        s3 += scaled(pv.w);
-      }
-    }
-    double s = warp_sum(bad ? static_cast<double>(NAN) : ((s0 + s1) + (s2 + s3)) * kUnscale);
+      return false;
+    });
+    double s = warp_sum(top >= kInvalid ? static_cast<double>(NAN) : ((s0 + s1) + (s2 + s3)) * kUnscale);
     ++pass;
     if (lane == 0) s_warp[pass & 1][warp] = s;
     __syncthreads();
@@ -211,31 +260,41 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(Params P) {
     for (int w = warp + 1; w < kWarps; ++w) after += s_warp[pass & 1][w];
     for (int k = rank + 1; k < C; ++k) after += s_cta[pass & 1][k];
     if (!(mine > 0.0 && target >= before && (target < hi || after == 0.0))) return -1;
-    const float* pr = prow0 + static_cast<int64_t>(c) * P.tp_st;
-    const float* qr = SAMPLED && a > 0.0 ? qrow0 + static_cast<int64_t>(c) * P.dp_st : nullptr;
-    int last = -1;
-    for (int es = e0; es < e1; es += 128) {
-      const int e = es + lane * 4;
-      float4 pv = make_float4(0.f, 0.f, 0.f, 0.f), qv = pv;
-      if (e < e1) pv = load4(pr, e, e1, vec, 0.f);
-      if (e < e1 && qr) qv = load4(qr, e, e1, vec, 0.f);
-      const double w0 = weight(pv.x, qv.x, a), w1 = weight(pv.y, qv.y, a);
-      const double w2 = weight(pv.z, qv.z, a), w3 = weight(pv.w, qv.w, a);
-      const double incl = warp_incl_scan((w0 + w1) + (w2 + w3));
-      const double c0 = before + (incl - ((w0 + w1) + (w2 + w3)));
-      int hit = -1;
-      if (w3 > 0.0 && c0 + w0 + w1 + w2 + w3 > target) hit = e + 3;
-      if (w2 > 0.0 && c0 + w0 + w1 + w2 > target) hit = e + 2;
-      if (w1 > 0.0 && c0 + w0 + w1 > target) hit = e + 1;
-      if (w0 > 0.0 && c0 + w0 > target) hit = e;
-      const unsigned m = __ballot_sync(0xffffffffu, hit >= 0);
-      if (m) return __shfl_sync(0xffffffffu, hit, __ffs(m) - 1);
-      const int pos = w3 > 0.0 ? e + 3 : (w2 > 0.0 ? e + 2 : (w1 > 0.0 ? e + 1 : (w0 > 0.0 ? e : -1)));
-      const unsigned z = __ballot_sync(0xffffffffu, pos >= 0);
-      if (z) last = __shfl_sync(0xffffffffu, pos, 31 - __clz(z));
+    // Lane l takes the l-th run of consecutive elements, so one scan over the
+    // lanes finds the run, and the whole warp then goes through that one run.
+    const bool with_q = SAMPLED && a > 0.0;
+    auto at = [&](int o) -> double {
+      return weight_scaled(prob_bits(buf_p[o]), with_q ? prob_bits(buf_q[o]) : 0u, a) * kUnscale;
+    };
+    int last = -1, hit_at = -1;
+    pieces(c, with_q, [&](int es, int ee) {
+      const int run = ((ee - es + 31) / 32) | 1;   // odd: the lanes' reads fall in 32 banks
+      double mine_sum = 0.0;
+      for (int o = lane * run; o < min(ee - es, (lane + 1) * run); ++o) mine_sum += at(o);
+      const double incl = warp_incl_scan(mine_sum);
+      const unsigned over = __ballot_sync(0xffffffffu, mine_sum > 0.0 && before + incl > target);
+      const unsigned some = __ballot_sync(0xffffffffu, mine_sum > 0.0);
+      if (some == 0u) return false;
+      // the run that holds the target, or (rounding, or it lies in a later piece) the last one with weight
+      const int l = over ? __ffs(over) - 1 : 31 - __clz(some);
+      double c0 = before + __shfl_sync(0xffffffffu, incl - mine_sum, l);
+      for (int o0 = l * run; o0 < min(ee - es, (l + 1) * run); o0 += 32) {
+        const int o = o0 + lane;
+        const double w = o < min(ee - es, (l + 1) * run) ? at(o) : 0.0;
+        const double in = warp_incl_scan(w);
+        const unsigned hit = __ballot_sync(0xffffffffu, w > 0.0 && c0 + in > target);
+        const unsigned pos = __ballot_sync(0xffffffffu, w > 0.0);
+        if (pos) last = es + o0 + 31 - __clz(pos);
+        if (hit) {
+          hit_at = es + o0 + __ffs(hit) - 1;
+          return true;
+        }
+        c0 += __shfl_sync(0xffffffffu, in, 31);
+      }
       before += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    return last;
+      return over != 0u;
+    });
+    return hit_at >= 0 ? hit_at : last;
   };
   // first child of c after node `from` (every warp by itself)
   auto next_child = [&](int c, int from) -> int {
@@ -333,9 +392,16 @@ cudaError_t launch_accept_probs(const tv_accept_probs_args* a, bool sampled, cud
   while (c > 1 && (static_cast<int64_t>(a->B) * c > 2 * num_sms() || a->V < c * kThreads * 4)) c /= 2;
   const int64_t per = (static_cast<int64_t>(a->V) + c * kWarps - 1) / (c * kWarps);
   p.chunk = static_cast<int>((per + 127) / 128 * 128);
-  const size_t smem = static_cast<size_t>(a->T) * (sampled ? 24 : 8);
+  // the whole chunk in shared memory where it fits (V up to about 200000 at
+  // 8 CTAs), else pieces of it
+  const size_t nodes = (static_cast<size_t>(a->T) * (sampled ? 24 : 8) + 15) / 16 * 16;
+  const size_t per_elt = static_cast<size_t>(kWarps) * (sampled ? 8 : 4);
+  const int fit = static_cast<int>((kMaxSmem - nodes) / per_elt) / 128 * 128;
+  p.cap = std::min(p.chunk, fit);
+  p.rows_at = static_cast<int>(nodes);
+  const size_t smem = nodes + static_cast<size_t>(p.cap) * per_elt;
   auto kernel = sampled ? accept_probs_kernel<true> : accept_probs_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxT * 24);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a->B) * c);
