@@ -6,7 +6,10 @@
 // rows); its key tiles are the prefix tiles of its sequence, then the tree
 // tiles.  All units' key tiles lie in one line, sequence by sequence, and
 // each CTA of a grid of about one CTA per SM takes an equal stretch of it:
-// a piece of a unit at either end, whole units between.  The line's length
+// a piece of a unit at either end, whole units between.  (Where sequences
+// have several row tiles on the tensor cores, a team of CTAs takes a stretch
+// together, a row tile each, so that they read the same keys at the same
+// time and all but one find them in the L2.)  The line's length
 // and every CTA's stretch follow from prefix_len and n_nodes on the device,
 // so ragged batches are balanced to one tile, a long table costs nothing,
 // and a single long sequence fills the GPU.  A unit that crosses stretches
@@ -39,14 +42,15 @@ struct PagedAttnParams {
   uint32_t* status;
   int prefix_only;
   int rows;                    // query rows of a unit
+  int team;                    // CTAs that share a stretch, each with one row tile of its units
   int box;                     // tensor cores: rows of a page that one TMA box takes (0: row by row)
-  float* part_o;               // [CTA][2][rows][d]: the CTA's piece that continues a unit, that begins one
-  float* part_lse;             // [CTA][2][rows], log2 units
-  struct SplitUnit* splits;    // [CTA] the unit that begins in that CTA and ends in a later one
+  float* part_o;               // [stretch][2][rows][d]: the piece that continues a unit, the one that begins one
+  float* part_lse;             // [stretch][2][rows], log2 units
+  struct SplitUnit* splits;    // [stretch] the unit that begins in it and ends in a later one
 };
 
-// A unit in pieces: it begins in CTA c0 (the CTA's second slot) and goes on
-// in c0 + 1 .. c1 (their first); c1 < 0: none.
+// A unit in pieces: it begins in stretch c0 (the second slot) and goes on in
+// c0 + 1 .. c1 (their first); c1 < 0: none.
 struct SplitUnit {
   int32_t c1, b, g, packed0, rows;
 };
@@ -99,6 +103,7 @@ struct Line {
   int nslot;
   int first, last;             // this CTA's stretch
   int step;                    // tiles of a stretch
+  int stretch;                 // this CTA's
 };
 
 // Called by all NT threads of the CTA (NT <= kMaxSlots, a multiple of 32).
@@ -138,9 +143,11 @@ __device__ __forceinline__ void build_line(const PagedAttnParams& p, Line& ln, i
     ln.cum[NT] = total;
     ln.per = per;
     ln.nslot = NT;
-    const int step = max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+    const int n = static_cast<int>(gridDim.x) / p.team, c = static_cast<int>(blockIdx.x) / p.team;
+    const int step = max(1, (total + n - 1) / n);
     ln.step = step;
-    ln.first = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(step) * blockIdx.x));
+    ln.stretch = c;
+    ln.first = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(step) * c));
     ln.last = ln.first + min(step, total - ln.first);
   }
   __syncthreads();
@@ -212,8 +219,8 @@ cudaError_t launch_attn_paged_simt(const PagedAttnParams& p, int grid, cudaStrea
 // Combines the split units' rows.
 cudaError_t launch_attn_paged_merge(const PagedAttnParams& p, int grid, cudaStream_t stream);
 bool attn_paged_tc_supported(const tv_attn_paged_args* a);
-// Rows of a unit of the tensor-core kernel, and its TMA boxes.
-int attn_paged_tc_rows(const tv_attn_paged_args* a);
+// Row tiles of a unit of the tensor-core kernel (a CTA each), and its TMA boxes.
+int attn_paged_tc_team(const tv_attn_paged_args* a);
 int attn_paged_tc_box(int page_size);
 cudaError_t launch_attn_paged_tc(const PagedAttnParams& p, int grid, cudaStream_t stream);
 // Query rows of the CUDA-core kernel's row tile and its CTAs per SM.

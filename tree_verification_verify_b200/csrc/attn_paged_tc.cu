@@ -3,22 +3,18 @@
 //
 // A persistent CTA per SM works through its stretch of the line
 // (attn_paged.cuh).  A unit's query rows are the G heads of one kv head of
-// up to 128 / G nodes (one row tile), or of twice as many (PAIR: two row
-// tiles, so that every K/V tile serves 256 rows); its key tiles are 128
-// prefix rows, fetched page by page, then tree nodes 128 at a time from the
-// last ones down, masked per row by the row's root path.  The prefix's last
-// rows and a small tree share one tile.  Loads, products and softmax of
-// consecutive tiles overlap across the borders of units.
+// up to 128 / G nodes (a row tile), or of a team of CTAs' row tiles; its key
+// tiles are 128 prefix rows, fetched page by page, then tree nodes 128 at a
+// time from the last ones down, masked per row by the row's root path.  The
+// prefix's last rows and a small tree share one tile.  Loads, products and
+// softmax of consecutive tiles overlap across the borders of units.
 //
 // Warp roles (384 threads):
 //   warps 0-7  softmax and output: two warpgroups, a thread per query row
-//              (TMEM lane), each with an online softmax state and an
-//              accumulator of its own (O_0, O_1 in TMEM).  With one row tile
-//              they take the key tiles in turn and meet once per piece;
-//              with two (PAIR) group h has row tile h.  One group's
-//              exponentials run while the other waits for TMEM and barriers
-//              (both on halves of the same tile: 5000 cycles a tile, half of
-//              them waits; in turn: 2700).  Warps without a valid row skip
+//              (TMEM lane), that take the key tiles in turn, so that one
+//              group's exponentials run while the other waits for TMEM and
+//              barriers (both on halves of the same tile: 5000 cycles a
+//              tile, half of them waits).  Warps without a valid row skip
 //              the arithmetic (decoding: G of 128 rows are real);
 //   warp 8     K tiles, warp 10 V tiles.  Page sizes that are multiples of
 //              8 rows: one TMA box per run of rows that both the page and
@@ -27,14 +23,20 @@
 //              batch ahead.  Other page sizes: 16-byte cp.async per row
 //              into the same swizzled layout;
 //   warp 9     MMA: one thread polls what is ready and issues S = Q K^T up
-//              to two ahead or O_h += P V (P read from TMEM), so neither
-//              waits for the other's operands;
+//              to three tiles ahead or O += P V (P read from TMEM), so
+//              neither waits for the other's operands;
 //   warp 11    the pieces' descriptions, several ahead of their use (finding
 //              one takes a search and four divisions), Q and parent[].
-// Online softmax in base 2; O is rescaled only when a row's maximum grows by
-// more than 2^8 (P <= 256, exact in O / l).  P is rounded to bf16 for the
-// product with V (the tensor cores' operand type); sums use the unrounded
-// fp32 weights.
+// TMEM: three S buffers and one accumulator O.  The groups share O, and so
+// they share each row's reference maximum m: P = 2^(s - m).  The group with
+// tile j takes m over from the group with tile j - 1 (a barrier per pair of
+// warps that share rows), raises it only when the tile's maximum exceeds it
+// by more than 8 (P <= 2^8, exact in O / l) and then rescales O itself, once
+// P V of tile j - 1 is done.  (With an accumulator and a maximum per group
+// there is room for two S buffers only, and S of a group's next tile has to
+// wait for P V of its last one: 3900 cycles a tile with 128 rows.)  P is
+// rounded to bf16 for the product with V (the tensor cores' operand type);
+// sums use the unrounded fp32 weights.
 //
 // V of a tree tile may hold infinities or NaN in nodes that a row does not
 // see, and 0 * NaN would reach that row.  The softmax warps look the nodes'
@@ -66,17 +68,17 @@ constexpr int kMaxT = 2048;
 constexpr int kTreeBox = 8;                               // tree nodes of a TMA box
 constexpr uint32_t kHalfBytes = kRows * 128;              // 128 rows x 64 bf16
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;                // S buffers 128 apart, O_0 and O_1 128 apart
+constexpr int kSB = 3;                                    // S buffers, 128 columns each
+constexpr uint32_t kColS = 0, kColO = kSB * 128;
 constexpr uint16_t kRootMark = 0xFFFEu, kBadMark = 0xFFFFu;
 constexpr int kRing = 8, kAhead = 3;                      // descriptions kept, and made ahead
 
-// Shared memory: Q, the K and V rings, two parent[] buffers.  192 KB of
-// tiles: 96 KB of K (64 KB where there are two Q tiles) and 64 KB of V.
-template <int D, bool PAIR>
+// Shared memory: Q, the K and V rings (96 KB and 64 KB), two parent[] buffers.
+template <int D>
 struct Shape {
   static constexpr uint32_t kTile = D / 64 * kHalfBytes;  // bytes of a K, V or Q tile
-  static constexpr int kKS = (PAIR ? 2 : 3) * 128 / D, kVS = 2 * 128 / D;
-  static constexpr uint32_t kQ = 0, kK = (PAIR ? 2 : 1) * kTile, kV = kK + kKS * kTile, kPar = kV + kVS * kTile;
+  static constexpr int kKS = 3 * 128 / D, kVS = 2 * 128 / D;
+  static constexpr uint32_t kQ = 0, kK = kTile, kV = kK + kKS * kTile, kPar = kV + kVS * kTile;
   static constexpr uint32_t kBytes = kPar + 2 * kMaxT * 2;
 };
 
@@ -86,32 +88,31 @@ struct Desc {
   int valid;                    // 0: there are no more pieces
   int cnt;                      // na + ntr
   int index, queue;             // pieces before it, and those of them with tiles
-  int b, g, i0;                 // sequence, kv head, first node
-  int nodes;                    // nodes of the unit
+  int b, g, i0;                 // sequence, kv head, first node of this CTA's row tile
+  int nodes;                    // nodes of the row tile (0: none)
+  int unit_i0, unit_nodes;      // of the whole unit
   int n, L;                     // the sequence's nodes and prefix rows
   int a0, na, ntr, lo0;
   int rem, off;                 // the tree tile's prefix rows, and where its nodes begin
   int bad_len, whole, begins;
   int c1;                       // the CTA in which the unit ends
-  __device__ __forceinline__ int live_end(int r) const {   // rows of tile r up to the last key
-    if (r < na) return min(kKeys, L - (a0 + r) * kKeys);
-    return off + min(n - (lo0 - (r - na) * kKeys), kKeys - off);
-  }
 };
 
 struct Bars {
   uint64_t q_full, q_empty;
   uint64_t k_full[6], k_empty[6], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_full[2], pv_done[2];              // by group: S buffer, P, accumulator
-  uint64_t o_free[2];                                     // the accumulator of the last piece has been read
+  uint64_t s_full[kSB], p_full[kSB];                      // S and P buffers
+  uint64_t pv_done[2];                                    // P V, by tile parity
+  uint64_t dec[4][2];                                     // [warp & 3][group] the group's rows have their reference maximum
+  uint64_t o_full, o_free;                                // a piece's O is whole; it has been read
   uint64_t t_full[2], t_empty[2];                         // parent[] buffers
   uint64_t w_full[kRing], w_empty[kRing];                 // piece descriptions
-  uint64_t vfix;                                          // PAIR: group 0 has looked a tree tile over
   uint32_t tmem_base;
   int abort;
   int bad_piece[8];                                       // piece number + 1 that met a bad page
   uint32_t vbad[2][4][4];                                 // [group][its tree tile & 3] V rows with infinities or NaN
   Desc desc[kRing];
+  float m_ref[kRows];                                     // the rows' reference maxima
   float red_m[2][kRows], red_l[2][kRows];
   uint8_t red_nf[2][kRows];
 };
@@ -139,6 +140,30 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// Non-blocking tests of five barriers in one go: bit i is set when phase
+// (parity >> i) & 1 of b[i] is complete.  One after the other, each test took
+// its own 100 to 300 cycles (shared memory is busy with operands and tiles).
+__device__ __forceinline__ uint32_t mbar_test5(uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3, uint32_t b4,
+                                               uint32_t parity) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p<5>;\n\t.reg .u32 q<5>, v<5>;\n\t"
+      "and.b32 q0, %6, 1;\n\tbfe.u32 q1, %6, 1, 1;\n\tbfe.u32 q2, %6, 2, 1;\n\t"
+      "bfe.u32 q3, %6, 3, 1;\n\tbfe.u32 q4, %6, 4, 1;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p0, [%1], q0;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p1, [%2], q1;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p2, [%3], q2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p3, [%4], q3;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p4, [%5], q4;\n\t"
+      "selp.u32 v0, 1, 0, p0;\n\tselp.u32 v1, 2, 0, p1;\n\tselp.u32 v2, 4, 0, p2;\n\t"
+      "selp.u32 v3, 8, 0, p3;\n\tselp.u32 v4, 16, 0, p4;\n\t"
+      "or.b32 v0, v0, v1;\n\tor.b32 v2, v2, v3;\n\tor.b32 v0, v0, v4;\n\tor.b32 %0, v0, v2;\n\t}"
+      : "=r"(r)
+      : "r"(b0), "r"(b1), "r"(b2), "r"(b3), "r"(b4), "r"(parity)
+      : "memory");
+  return r;
 }
 
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
@@ -174,12 +199,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
 
 using namespace ptc;
 
-template <int D, bool PAIR>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_kt,
                      const __grid_constant__ CUtensorMap map_vt, PagedAttnParams p) {
-  using Sh = Shape<D, PAIR>;
+  using Sh = Shape<D>;
   constexpr int KS = Sh::kKS, VS = Sh::kVS;
   constexpr uint32_t TB = Sh::kTile;
   extern __shared__ uint8_t dsmem_raw[];
@@ -188,7 +213,8 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.G, box = p.box;
   const int align = box > 0 ? box : 8;
-  const int npt = (PAIR ? p.rows / 2 : p.rows) / G;       // nodes of a row tile
+  const int npt = p.rows / p.team / G;                    // nodes of a row tile
+  const int member = static_cast<int>(blockIdx.x) % p.team;
   const uint32_t raw = smem_u32(dsmem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;           // 128B swizzle atoms are 1 KB
   uint8_t* gbase = dsmem_raw + (base - raw);
@@ -203,16 +229,15 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     mbar_init(&bars.q_full, 1); mbar_init(&bars.q_empty, 1);
     for (int s = 0; s < KS; ++s) { mbar_init(&bars.k_full[s], 1); mbar_init(&bars.k_empty[s], 1); }
     for (int s = 0; s < VS; ++s) { mbar_init(&bars.v_full[s], 1); mbar_init(&bars.v_empty[s], 1); }
+    for (int s = 0; s < kSB; ++s) { mbar_init(&bars.s_full[s], 1); mbar_init(&bars.p_full[s], 4); }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars.s_full[s], 1);
-      mbar_init(&bars.p_full[s], 4);
       mbar_init(&bars.pv_done[s], 1);
-      mbar_init(&bars.o_free[s], PAIR ? 4 : 8);           // PAIR: a group reads its own accumulator alone
+      for (int i = 0; i < 4; ++i) mbar_init(&bars.dec[i][s], 1);
       mbar_init(&bars.t_full[s], 1); mbar_init(&bars.t_empty[s], 8);
       for (int i = 0; i < 16; ++i) bars.vbad[s][i >> 2][i & 3] = 0;
     }
+    mbar_init(&bars.o_full, 1); mbar_init(&bars.o_free, 8);
     for (int s = 0; s < kRing; ++s) { mbar_init(&bars.w_full[s], 1); mbar_init(&bars.w_empty[s], 11); }
-    mbar_init(&bars.vfix, 4);
     for (int i = 0; i < 8; ++i) bars.bad_piece[i] = 0;
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -404,19 +429,21 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       if (x.valid) {
         const Piece c = piece_at<kKeys>(p, ln, pos, align);
         pos += c.t1 - c.t0;
-        const int npu = PAIR ? 2 * npt : npt;             // nodes of a unit
-        x.b = c.b; x.g = c.g; x.i0 = c.rt * npu;
-        x.nodes = min(npu, c.s.n - x.i0);
+        x.unit_i0 = c.rt * npt * p.team;
+        x.unit_nodes = min(npt * p.team, c.s.n - x.unit_i0);
+        x.b = c.b; x.g = c.g; x.i0 = x.unit_i0 + member * npt;
+        x.nodes = max(0, min(npt, c.s.n - x.i0));
         x.n = c.s.n; x.L = c.s.L;
         x.a0 = min(c.t0, c.s.nprefix);
         x.na = min(c.t1, c.s.nprefix) - x.a0;
-        // tree tiles of later nodes than the unit's are left out
-        const int skip = c.s.ntree > 0 ? c.s.ntree - ((x.i0 + x.nodes - 1) / kKeys + 1) : 0;
+        // tree tiles of later nodes than the row tile's are left out
+        const int skip = c.s.ntree > 0 ? c.s.ntree - ((x.i0 + max(x.nodes, 1) - 1) / kKeys + 1) : 0;
         const int b0 = max(c.t0, c.s.nprefix + skip), b1 = min(c.t1, c.s.nprefix + c.s.ntree);
         x.ntr = max(0, b1 - b0);
         x.lo0 = (c.s.ntree - 1 - (b0 - c.s.nprefix)) * kKeys;
         x.rem = x.ntr > 0 ? c.s.rem : 0;
         x.off = x.ntr > 0 ? c.s.off : 0;
+        if (x.nodes == 0) x.na = x.ntr = 0;               // a team mate's row tile is the last
         x.cnt = x.na + x.ntr;
         x.index = made;
         x.queue = queue;
@@ -446,12 +473,10 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (!ok) return;
         if (lane == 0) {
           // rows past the tensor's nodes read as zeros
-          mbar_expect_tx(&bars.q_full, static_cast<uint32_t>(p.rows) * D * 2);
+          mbar_expect_tx(&bars.q_full, static_cast<uint32_t>(npt * G) * D * 2);
 #pragma unroll
-          for (int q = 0; q < (PAIR ? 2 : 1); ++q)
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-              tma_load_4d(&map_q, base + Sh::kQ + q * TB + h * kHalfBytes, &bars.q_full, 64 * h, d.g * G, d.i0 + q * npt, d.b);
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(&map_q, base + Sh::kQ + h * kHalfBytes, &bars.q_full, 64 * h, d.g * G, d.i0, d.b);
         }
         ++nq;
       };
@@ -480,74 +505,81 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr int SUB = PAIR ? 2 : 1;                   // products of a kind per key tile
       const uint32_t idesc_qk = instr_desc(kRows, kKeys, 0, 0);
       const uint32_t idesc_pv = instr_desc(kRows, D, 0, 1);
-      int is = 0, ip = 0;                                 // S and P V issued in all; number i is of group i & 1
+      int is = 0, ip = 0;                                 // S and P V issued in all
       int rs = 0, rp = 0;                                 // of those, in the present pieces
       int ks = -1, kp = -1;                               // the present pieces
       const Desc *ds = nullptr, *dp = nullptr;
-      auto next_s = [&]() { do ds = desc(++ks); while (ds && ds->cnt == 0); rs = 0; };
+      int cnt_s = 0, cnt_p = 0, queue_s = 0, queue_p = 0; // tiles of the present pieces, pieces before them
+      int na = 0, keys0 = 0, nodes = 0, lo0 = 0, off = 0; // of the piece of the next P V
+      auto next_s = [&]() {
+        do ds = desc(++ks); while (ds && ds->cnt == 0);
+        if (ds) {
+          cnt_s = ds->cnt;
+          queue_s = ds->queue;
+        }
+        rs = 0;
+      };
       auto next_p = [&]() {
         do {
           if (kp >= 0) release(kp);
           dp = desc(++kp);
         } while (dp && dp->cnt == 0);
+        if (dp) {
+          cnt_p = dp->cnt;
+          queue_p = dp->queue;
+          na = dp->na; keys0 = dp->L - dp->a0 * kKeys; nodes = dp->n; lo0 = dp->lo0; off = dp->off;
+        }
         rp = 0;
       };
       next_s();
       next_p();
       uint32_t idle = 0;
       while (dp) {
-        // all tests of a poll are independent: together they cost little more than one
-        const int tks = is / SUB, tvs = ip / SUB;
-        const bool want_s = ds && is < ip + 2;
-        const bool tk = want_s && mbar_test(&bars.k_full[tks % KS], (tks / KS) & 1);
-        const bool tq = want_s && (rs > 0 || mbar_test(&bars.q_full, ds->queue & 1));
-        const bool want_p = ip < is;
-        const bool tv = want_p && mbar_test(&bars.v_full[tvs % VS], (tvs / VS) & 1);
-        const bool tp = want_p && mbar_test(&bars.p_full[ip & 1], (ip >> 1) & 1);
-        // the first product of either group overwrites its accumulator, so the last piece's must have been read
-        const bool to = want_p && (rp > 1 || dp->queue == 0 || mbar_test(&bars.o_free[ip & 1], (dp->queue - 1) & 1));
+        const uint32_t par = static_cast<uint32_t>((is / KS) & 1) | static_cast<uint32_t>(queue_s & 1) << 1 |
+                             static_cast<uint32_t>((ip / VS) & 1) << 2 | static_cast<uint32_t>((ip / kSB) & 1) << 3 |
+                             static_cast<uint32_t>((queue_p - 1) & 1) << 4;
+        const uint32_t got = mbar_test5(smem_u32(&bars.k_full[is % KS]), smem_u32(&bars.q_full), smem_u32(&bars.v_full[ip % VS]),
+                                        smem_u32(&bars.p_full[ip % kSB]), smem_u32(&bars.o_free), par);
+        const bool want_s = ds && is < ip + kSB, want_p = ip < is;
         bool did = false;
-        if (tk && tq) {
+        // O += P V: P is bf16 pairs over the first 64 columns of its S.  The
+        // first product of a piece overwrites O, so the last piece's must have been read.
+        if (want_p && (got & 12u) == 12u && (rp > 0 || queue_p == 0 || (got & 16u))) {
           fence_after();
-          const uint32_t sq = base + Sh::kQ + (PAIR ? (is & 1) * TB : 0), sk = base + Sh::kK + (tks % KS) * TB;
-          const uint32_t sd = tmem + kColS + (is & 1) * 128;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-            mma_bf16(sd, smem_desc(sq + o, 16, 1024), smem_desc(sk + o, 16, 1024), idesc_qk, kk > 0);
-          }
-          if (!PAIR || (is & 1)) mma_commit(&bars.k_empty[tks % KS]);
-          mma_commit(&bars.s_full[is & 1]);
-          ++is;
-          if (++rs == ds->cnt * SUB) {
-            mma_commit(&bars.q_empty);
-            next_s();
+          const uint64_t dv = smem_desc(base + Sh::kV + (ip % VS) * TB, kHalfBytes, 1024);
+          const uint32_t od = tmem + kColO, pd = tmem + kColS + (ip % kSB) * 128;
+          const int end = rp < na ? min(kKeys, keys0 - rp * kKeys) : off + min(nodes - (lo0 - (rp - na) * kKeys), kKeys - off);
+          const int steps = (end + 15) / 16;              // K steps up to the tile's last key
+#pragma unroll 1
+          for (int kk = 0; kk < steps; ++kk)              // (16 rows of V are 2 KB)
+            mma_bf16_ts(od, pd + kk * 8, dv + kk * 128, idesc_pv, (rp > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&bars.v_empty[ip % VS]);
+          mma_commit(&bars.pv_done[ip & 1]);
+          ++ip;
+          if (++rp == cnt_p) {
+            mma_commit(&bars.o_full);
+            next_p();
           }
           did = true;
         }
-        // O_h += P V: P is bf16 pairs over the first 64 columns of its S
-        if (tv && tp && to) {
+        if (want_s && (got & 1u) && (rs > 0 || (got & 2u))) {
           fence_after();
-          const uint32_t sv = base + Sh::kV + (tvs % VS) * TB;
-          const uint32_t od = tmem + kColO + (ip & 1) * 128, pd = tmem + kColS + (ip & 1) * 128;
-          const int steps = (dp->live_end(rp / SUB) + 15) / 16;
-          if (steps == 8) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ts(od, pd + kk * 8, smem_desc(sv + kk * 2048, kHalfBytes, 1024), idesc_pv,
-                          (rp > 1 || kk > 0) ? 1u : 0u);
-          } else {
-            for (int kk = 0; kk < steps; ++kk)
-              mma_bf16_ts(od, pd + kk * 8, smem_desc(sv + kk * 2048, kHalfBytes, 1024), idesc_pv,
-                          (rp > 1 || kk > 0) ? 1u : 0u);
+          const uint64_t dq = smem_desc(base + Sh::kQ, 16, 1024), dk = smem_desc(base + Sh::kK + (is % KS) * TB, 16, 1024);
+          const uint32_t sd = tmem + kColS + (is % kSB) * 128;
+#pragma unroll 1
+          for (int kk = 0; kk < D / 16; ++kk) {           // (16 columns are 32 B, 64 a half tile)
+            const uint32_t o = (kk >> 2) * (kHalfBytes >> 4) + (kk & 3) * 2;
+            mma_bf16(sd, dq + o, dk + o, idesc_qk, kk > 0);
           }
-          if (!PAIR || (ip & 1)) mma_commit(&bars.v_empty[tvs % VS]);
-          mma_commit(&bars.pv_done[ip & 1]);
-          ++ip;
-          if (++rp == dp->cnt * SUB) next_p();
+          mma_commit(&bars.k_empty[is % KS]);
+          mma_commit(&bars.s_full[is % kSB]);
+          ++is;
+          if (++rs == cnt_s) {
+            mma_commit(&bars.q_empty);
+            next_s();
+          }
           did = true;
         }
         if (did) {
@@ -559,7 +591,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       }
       if (*abort) {
         // what was issued completes before the TMEM is freed
-        for (int j = is > 2 ? is - 2 : 0; j < is; ++j) mbar_drain(&bars.s_full[j & 1], (j >> 1) & 1);
+        for (int j = is > kSB ? is - kSB : 0; j < is; ++j) mbar_drain(&bars.s_full[j % kSB], (j / kSB) & 1);
         for (int j = ip > 2 ? ip - 2 : 0; j < ip; ++j) mbar_drain(&bars.pv_done[j & 1], (j >> 1) & 1);
         while (dp) next_p();
       }
@@ -571,29 +603,27 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     const int row = tid & (kRows - 1), half = tid >> 7;   // half: the warpgroup
     const float sl2 = p.scale * 1.4426950408889634f;      // scores in log2 units
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t scol = trow + kColS + 128u * static_cast<uint32_t>(half);
-    const uint32_t ocol = trow + kColO + 128u * static_cast<uint32_t>(half);
-    int it0 = 0, ntree = 0, nfix = 0;                     // tiles, tree pieces, tree tiles of the group before this piece
+    const uint32_t ocol = trow + kColO;
+    int it0 = 0, ntree = 0, nfix = 0;                     // tiles, tree pieces, the group's tree tiles before this piece
+    int nout = 0;                                         // pieces with tiles before this one
     SplitUnit split = {-1, 0, 0, 0, 0};
     bool ok = true;
     for (int k = 0;; ++k) {
       const Desc* d = desc(k);
       if (!d) break;
-      const int first = PAIR ? half * npt : 0;            // the group's first node of the unit
-      const int my_rows = min(PAIR ? npt : p.rows / G, d->nodes - first) * G;
+      const int my_rows = d->nodes * G;
       const bool live = (warp & 3) * 32 < my_rows;        // the warp has valid rows
       const bool row_valid = row < my_rows;
-      const int my_node = d->i0 + first + row / G;
+      const int my_node = d->i0 + row / G;
       const int na = d->na, cnt = d->cnt, nodes = d->n, rem = d->rem, off = d->off, lo0 = d->lo0;
       const int keys0 = d->L - d->a0 * kKeys;             // prefix keys from the piece's first tile on
-      const int r0 = PAIR ? 0 : (half ^ it0) & 1;         // the group's first tile
-      float m_run = -INFINITY, l_run = 0.f;
+      float m_run = -INFINITY, l_run = 0.f;               // the maximum that l_run refers to
       bool my_ok = true, nf = false;
       int cur = -2;                                       // walk position on this row's root path (-2: not begun)
       const uint16_t* par = spar + (ntree & 1) * kMaxT;
-      for (int r = r0; r < cnt; r += PAIR ? 1 : 2) {
-        const int it = it0 + r;
-        const uint32_t phase = static_cast<uint32_t>(PAIR ? it : it >> 1) & 1u;
+      for (int r = (half ^ it0) & 1; r < cnt; r += 2) {
+        const int it = it0 + r, sb = it % kSB;
+        const uint32_t scol = trow + kColS + 128u * static_cast<uint32_t>(sb);
         const bool tree = r >= na;
         const int lo = lo0 - (r - na) * kKeys;            // tree tile: its first node
         // keys [0, np) of the prefix, [off, end) of the tree
@@ -623,7 +653,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             cur = up >= kRootMark ? -1 : static_cast<int>(up);
           }
         }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.s_full[half], phase, abort));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.s_full[sb], (it / kSB) & 1, abort));
         fence_after();
         if (live && ok) {
           float s[128];
@@ -634,16 +664,43 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 #pragma unroll
             for (int x = 0; x < 128; ++x) s[x] = ((mk[x >> 5] >> (x & 31)) & 1u) ? s[x] : -INFINITY;
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float mx[8];
 #pragma unroll
-          for (int x = 0; x < 128; x += 2) mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], s[x], s[x + 1]);
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-          const float m_new = fmaxf(m_run, mt);
-          const bool grow = m_new > m_run + 8.0f;         // also the first finite maximum
-          float factor = 1.f;
-          if (grow) {
-            factor = ex2_approx(m_run - m_new);           // 0 when m_run = -inf
-            m_run = m_new;
+          for (int x = 0; x < 8; ++x) mx[x] = fmaxf(s[x], s[x + 8]);
+#pragma unroll
+          for (int x = 16; x < 128; x += 2) mx[(x >> 1) & 7] = max3(mx[(x >> 1) & 7], s[x], s[x + 1]);
+          const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sl2;
+          // the row's reference maximum after the tile before
+          float m = -INFINITY;
+          if (r > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars.dec[warp & 3][half ^ 1], ((it - 1) >> 1) & 1, abort));
+            m = bars.m_ref[row];
+          }
+          const float m_new = fmaxf(m, mt);
+          const bool grow = m_new > m + 8.0f;             // also the first finite maximum
+          if (__any_sync(0xffffffffu, grow) && r > 0 && ok) {
+            // O holds the tiles before this one: wait for the last P V, then rescale
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort));
+            fence_after();
+            const float factor = grow ? ex2_approx(m - m_new) : 1.f;   // 0 when m = -inf
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              float o[16];
+              tmem_ld16(ocol + q * 16, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= factor;
+              tmem_st16(ocol + q * 16, o);
+            }
+            tmem_wait_st();
+          }
+          if (grow) m = m_new;
+          if (grow || r == 0) bars.m_ref[row] = m;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.dec[warp & 3][half]);
+          if (m != m_run) {
+            l_run = m_run == -INFINITY ? 0.f : l_run * ex2_approx(m_run - m);
+            m_run = m;
           }
           const float nmu = (m_run == -INFINITY) ? 0.f : -m_run;
           // p = 2^(s sl2 - m) as bf16 pairs over the first half of S
@@ -663,23 +720,12 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             tmem_st16u(scol + q * 16, pk);
           }
           const float2 sum = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
-          l_run = l_run * factor + (sum.x + sum.y);
-          if (__any_sync(0xffffffffu, grow) && r > r0) {
-            // O_h holds the group's tiles before this one (their P V is done:
-            // this tile's S was issued behind it): rescale
-#pragma unroll 1
-            for (int q = 0; q < D / 16; ++q) {
-              float o[16];
-              tmem_ld16(ocol + q * 16, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] *= factor;
-              tmem_st16(ocol + q * 16, o);
-            }
-          }
+          l_run += sum.x + sum.y;
           tmem_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(&bars.dec[warp & 3][half]);
         }
-        if (!full && (!PAIR || half == 0)) {
+        if (!full) {
           // V rows of the K steps that are no keys are cleared, nodes' rows looked over
           ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.v_full[it % VS], (it / VS) & 1, abort));
           uint8_t* v0 = gbase + Sh::kV + (it % VS) * TB;
@@ -716,80 +762,57 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           // every warp of the group comes here for every tree tile, after an abort too
           if (tree) bar_sync(2 + half, 128);
-          if (PAIR && tree && lane == 0) mbar_arrive(&bars.vfix);
         }
         if (tree) {
-          if (PAIR && half == 1) ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.vfix, nfix & 1, abort));
-          const volatile uint32_t* vbad = bars.vbad[PAIR ? 0 : half][nfix & 3];
+          const volatile uint32_t* vbad = bars.vbad[half][nfix & 3];
 #pragma unroll
           for (int i = 0; i < 4; ++i) nf = nf || (vbad[i] & mk[i]);
           // the slot after next was last read two tree tiles ago
-          if ((!PAIR || half == 0) && (tid & 127) < 4) bars.vbad[half][(nfix + 2) & 3][tid & 3] = 0;
+          if ((tid & 127) < 4) bars.vbad[half][(nfix + 2) & 3][tid & 3] = 0;
           ++nfix;
         }
         fence_before();
         __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(&bars.p_full[half]);
+        if (lane == 0 && ok) mbar_arrive(&bars.p_full[sb]);
       }
       // ---------------------------------------------------------- output
-      const int g0 = it0 & 1;                             // (one row tile) the group of the piece's first tile
       it0 += cnt;
-      if (cnt > r0) {
-        // the group's last P V
-        const int last = PAIR ? it0 - 1 : (it0 - 1 - ((it0 - 1 - half) & 1)) >> 1;
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.pv_done[half], static_cast<uint32_t>(last) & 1u, abort));
-      }
+      if (cnt > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.o_full, nout & 1, abort));
+      // the groups' sums meet at the larger of their maxima, O's reference:
+      // out = O / (2^(m_0 - M) l_0 + 2^(m_1 - M) l_1); group h writes half of the columns
+      bars.red_m[half][row] = m_run;
+      bars.red_l[half][row] = l_run;
+      bars.red_nf[half][row] = nf + 2 * !my_ok;
+      bar_sync(1, kSoftmaxThreads);
       fence_after();
-      float c_0, c_1, M, l_row;                           // weights of O_0, O_1; maximum and sum
-      bool have_0, have_1;                                // accumulators that hold something
-      if (PAIR) {
-        have_0 = cnt > 0 && half == 0;
-        have_1 = cnt > 0 && half == 1;
-        c_0 = c_1 = 1.f;
-        M = m_run;
-        l_row = l_run;
-      } else {
-        // the groups meet: M = max(m_0, m_1), c_h = 2^(m_h - M),
-        // O = (c_0 O_0 + c_1 O_1) / (c_0 l_0 + c_1 l_1); group h writes half of the columns
-        bars.red_m[half][row] = m_run;
-        bars.red_l[half][row] = l_run;
-        bars.red_nf[half][row] = nf + 2 * !my_ok;
-        fence_before();
-        bar_sync(1, kSoftmaxThreads);
-        fence_after();
-        const float m_0 = bars.red_m[0][row], m_1 = bars.red_m[1][row];
-        const float l_0 = bars.red_l[0][row], l_1 = bars.red_l[1][row];
-        nf = ((bars.red_nf[0][row] | bars.red_nf[1][row]) & 1) != 0;
-        my_ok = ((bars.red_nf[0][row] | bars.red_nf[1][row]) & 2) == 0;
-        M = fmaxf(m_0, m_1);
-        c_0 = (m_0 == -INFINITY) ? 0.f : ex2_approx(m_0 - M);
-        c_1 = (m_1 == -INFINITY) ? 0.f : ex2_approx(m_1 - M);
-        // a group whose sum is NaN (a NaN score) makes the row NaN
-        l_row = c_0 * l_0 + c_1 * l_1 + ((l_0 != l_0 || l_1 != l_1) ? NAN : 0.f);
-        have_0 = cnt > g0;
-        have_1 = cnt > 1 - g0;
-      }
+      const float m_0 = bars.red_m[0][row], m_1 = bars.red_m[1][row];
+      const float l_0 = bars.red_l[0][row], l_1 = bars.red_l[1][row];
+      nf = ((bars.red_nf[0][row] | bars.red_nf[1][row]) & 1) != 0;
+      my_ok = ((bars.red_nf[0][row] | bars.red_nf[1][row]) & 2) == 0;
+      const float M = fmaxf(m_0, m_1);
+      const float c_0 = (m_0 == -INFINITY) ? 0.f : ex2_approx(m_0 - M);
+      const float c_1 = (m_1 == -INFINITY) ? 0.f : ex2_approx(m_1 - M);
+      // a group whose sum is NaN (a NaN score) makes the row NaN
+      const float l_row = c_0 * l_0 + c_1 * l_1 + ((l_0 != l_0 || l_1 != l_1) ? NAN : 0.f);
       const bool bad = d->bad_len || !my_ok || !ok || bars.bad_piece[d->index & 7] == d->index + 1;
       const bool empty = l_row == 0.f;
       const float inv = bad ? NAN : (empty ? 0.f : 1.f / l_row);
-      const float w_0 = c_0 * inv, w_1 = c_1 * inv;
       const bool whole = d->whole;
-      const int packed = (d->i0 + first) * G + row;
-      const int64_t slot = part_slot(p, blockIdx.x, d->begins ? 1 : 0) + first * G + row;
+      const int packed = d->i0 * G + row;
+      const int64_t slot = part_slot(p, ln.stretch, d->begins ? 1 : 0) + member * npt * G + row;
       if (live) {
         __nv_bfloat16* orow = row_valid ? out_row<__nv_bfloat16>(p, d->b, d->g, packed) : nullptr;
-        constexpr int NC = PAIR ? D : D / 2;              // columns of a thread
+        constexpr int NC = D / 2;                         // columns of a thread
 #pragma unroll 1
         for (int q = 0; q < NC / 32; ++q) {
-          const int col = (PAIR ? 0 : half * NC) + q * 32;
-          float v0[32], v1[32];
-          if (have_0) tmem_ld32(trow + kColO + col, v0);
-          if (have_1) tmem_ld32(trow + kColO + 128 + col, v1);
+          const int col = half * NC + q * 32;
+          float v0[32];
+          tmem_ld32(ocol + col, v0);
           tmem_wait_ld();
           if (!row_valid) continue;
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            v0[e] = (have_0 ? w_0 * v0[e] : 0.f) + (have_1 ? w_1 * v1[e] : 0.f) + (bad ? NAN : 0.f);
+            v0[e] = bad ? NAN : (empty ? 0.f : v0[e] * inv);
           if (nf) {
             // the values that are not finite, of the nodes this row sees
             int j = my_node;
@@ -823,23 +846,19 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                   make_float4(v0[4 * e], v0[4 * e + 1], v0[4 * e + 2], v0[4 * e + 3]);
           }
         }
-        if ((PAIR || half == 0) && row_valid) {
+        if (half == 0 && row_valid) {
           const float lse2 = bad ? NAN : (empty ? -INFINITY : M + log2f(l_row));
           if (!whole) p.part_lse[slot] = lse2;
           else if (p.lse) p.lse[lse_row(p, d->b, d->g, packed)] = lse2 * kLn2;
           if (!my_ok) set_status(p.status, TV_DEV_BAD_PARENT);
         }
       }
-      // the accumulators and parent[] are free for the pieces to come
+      // O and parent[] are free for the pieces to come
       fence_before();
       __syncwarp();
-      if (lane == 0 && cnt > 0) {
-        if (PAIR) {
-          mbar_arrive(&bars.o_free[half]);
-        } else {
-          mbar_arrive(&bars.o_free[0]);
-          mbar_arrive(&bars.o_free[1]);
-        }
+      if (cnt > 0) {
+        if (lane == 0) mbar_arrive(&bars.o_free);
+        ++nout;
       }
       if (d->ntr > 0) {
         if (lane == 0) mbar_arrive(&bars.t_empty[ntree & 1]);
@@ -848,13 +867,13 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       if (tid == 0) {
         if (bars.bad_piece[d->index & 7] == d->index + 1) set_status(p.status, TV_DEV_BAD_PAGE);
         if (!ok) set_status(p.status, TV_DEV_TIMEOUT);
-        if (d->begins && !whole) split = SplitUnit{d->c1, d->b, d->g, d->i0 * G, d->nodes * G};
+        if (d->begins && !whole) split = SplitUnit{d->c1, d->b, d->g, d->unit_i0 * G, d->unit_nodes * G};
       }
-      if (!PAIR) bar_sync(1, kSoftmaxThreads);            // red_*: read by all
+      bar_sync(1, kSoftmaxThreads);                       // red_*, m_ref: read by all
       __syncwarp();
       if (lane == 0) release(k);
     }
-    if (tid == 0) p.splits[blockIdx.x] = split;
+    if (tid == 0 && member == 0) p.splits[ln.stretch] = split;
   }
   fence_before();
   __syncthreads();
@@ -872,13 +891,13 @@ int64_t stride_or(int64_t dim, int64_t s) { return dim > 1 ? s : 128; }
 
 bool stride_ok(int64_t dim, int64_t s) { return dim <= 1 || (s > 0 && s % 8 == 0 && s * 2 < (1ll << 40)); }
 
-template <int D, bool PAIR>
+template <int D>
 cudaError_t launch(const PagedAttnParams& p, int grid, const CUtensorMap* m, cudaStream_t stream) {
-  constexpr size_t smem = Shape<D, PAIR>::kBytes + 1024;
-  const cudaError_t e = cudaFuncSetAttribute(attn_paged_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  constexpr size_t smem = Shape<D>::kBytes + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(attn_paged_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  attn_paged_tc_kernel<D, PAIR><<<grid, kThreads, smem, stream>>>(m[0], m[1], m[2], m[3], m[4], p);
+  attn_paged_tc_kernel<D><<<grid, kThreads, smem, stream>>>(m[0], m[1], m[2], m[3], m[4], p);
   return cudaGetLastError();
 }
 
@@ -890,10 +909,12 @@ int attn_paged_tc_box(int P) {
   return b >= 8 ? b : 0;
 }
 
-// One row tile, or two where a sequence can have more rows than one holds.
-int attn_paged_tc_rows(const tv_attn_paged_args* a) {
-  const int G = a->Hq / a->Hkv, tile = kRows / G * G;
-  return static_cast<int64_t>(a->T) * G > tile ? 2 * tile : tile;
+// As many CTAs to a team as a sequence can have row tiles, four at most (then
+// the other row tiles read the keys again).
+int attn_paged_tc_team(const tv_attn_paged_args* a) {
+  const int G = a->Hq / a->Hkv, npt = kRows / G;
+  const int tiles = (a->T + npt - 1) / npt;
+  return tiles > 2 ? 4 : tiles;
 }
 
 bool attn_paged_tc_supported(const tv_attn_paged_args* a) {
@@ -928,9 +949,7 @@ cudaError_t launch_attn_paged_tc(const PagedAttnParams& p, int grid, cudaStream_
     m[1] = m[3];
     m[2] = m[4];
   }
-  const bool pair = p.rows > tile;
-  if (p.d == 64) return pair ? launch<64, true>(p, grid, m, stream) : launch<64, false>(p, grid, m, stream);
-  return pair ? launch<128, true>(p, grid, m, stream) : launch<128, false>(p, grid, m, stream);
+  return p.d == 64 ? launch<64>(p, grid, m, stream) : launch<128>(p, grid, m, stream);
 }
 
 }  // namespace tv

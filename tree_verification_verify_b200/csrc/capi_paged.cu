@@ -2,6 +2,7 @@
 // tree_accept_probs, tree_commit_kv_paged, tree_pages_update,
 // tree_pages_compact): host-side argument checks, workspace layout and
 // dispatch.  Declared in include/tree_verify.h.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -74,7 +75,7 @@ tv_status check_attn_paged(const tv_attn_paged_args* a) {
 
 struct PagedPlan {
   bool tc;
-  int rows, grid;
+  int rows, team, grid;        // grid: stretches times team
   bool fits;                   // the line has fewer than 2^31 key tiles
   size_t off_o, off_lse, off_splits, total;
 };
@@ -83,7 +84,8 @@ PagedPlan plan_attn_paged(const tv_attn_paged_args* a) {
   PagedPlan pl;
   const int G = a->Hq / a->Hkv;
   pl.tc = attn_paged_tc_supported(a);
-  pl.rows = pl.tc ? attn_paged_tc_rows(a) : attn_paged_simt_rows(static_cast<int64_t>(a->T) * G);
+  pl.team = pl.tc ? attn_paged_tc_team(a) : 1;
+  pl.rows = pl.tc ? 128 / G * G * pl.team : attn_paged_simt_rows(static_cast<int64_t>(a->T) * G);
   const int keys = pl.tc ? 128 : 64;
   // no more CTAs than key tiles can be
   const int64_t rt = (static_cast<int64_t>(a->T) * G + pl.rows - 1) / pl.rows;
@@ -91,8 +93,9 @@ PagedPlan plan_attn_paged(const tv_attn_paged_args* a) {
   const int64_t most = static_cast<int64_t>(a->B) * a->Hkv * rt * (tiles > 0 ? tiles : 1);
   pl.fits = most < (1ll << 31);
   const int64_t want = static_cast<int64_t>(num_sms()) * (pl.tc ? 1 : attn_paged_simt_ctas(pl.rows, a->d));
-  pl.grid = static_cast<int>(most < want ? (most > 0 ? most : 1) : want);
-  const size_t slots = static_cast<size_t>(pl.grid) * 2 * pl.rows;
+  const int64_t stretches = std::max<int64_t>(1, std::min(most, want / pl.team));
+  pl.grid = static_cast<int>(stretches * pl.team);
+  const size_t slots = static_cast<size_t>(stretches) * 2 * pl.rows;
   size_t off = kTicketBytes;
   pl.off_o = off;   off = align256(off + slots * a->d * sizeof(float));
   pl.off_lse = off; off = align256(off + slots * sizeof(float));
@@ -140,7 +143,7 @@ extern "C" tv_status tree_verify_attn_paged(const tv_attn_paged_args* a, void* w
   p.lse = a->lse;
   p.status = a->dev_status;
   p.prefix_only = a->prefix_only;
-  p.rows = pl.rows;
+  p.rows = pl.rows; p.team = pl.team;
   p.box = pl.tc ? attn_paged_tc_box(a->page_size) : 0;
   unsigned char* w = static_cast<unsigned char*>(ws);
   p.splits = reinterpret_cast<SplitUnit*>(w + pl.off_splits);
@@ -149,7 +152,7 @@ extern "C" tv_status tree_verify_attn_paged(const tv_attn_paged_args* a, void* w
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = pl.tc ? launch_attn_paged_tc(p, pl.grid, s) : launch_attn_paged_simt(p, pl.grid, s);
   if (e != cudaSuccess) return TV_ERR_CUDA;
-  return from_cuda(launch_attn_paged_merge(p, pl.grid, s));
+  return from_cuda(launch_attn_paged_merge(p, pl.grid / pl.team, s));
 }
 
 // ------------------------------------------------------------ acceptance
