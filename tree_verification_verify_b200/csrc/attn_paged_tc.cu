@@ -552,9 +552,16 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           const uint32_t od = tmem + kColO, pd = tmem + kColS + (ip % kSB) * 128;
           const int end = rp < na ? min(kKeys, keys0 - rp * kKeys) : off + min(nodes - (lo0 - (rp - na) * kKeys), kKeys - off);
           const int steps = (end + 15) / 16;              // K steps up to the tile's last key
+          // (16 rows of V are 2 KB; unrolled for the tiles that count: issued
+          // from a loop, a tile's 8 MMAs took 1000 cycles instead of 550)
+          if (steps == 8) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) mma_bf16_ts(od, pd + kk * 8, dv + kk * 128, idesc_pv, (rp > 0 || kk > 0) ? 1u : 0u);
+          } else {
 #pragma unroll 1
-          for (int kk = 0; kk < steps; ++kk)              // (16 rows of V are 2 KB)
-            mma_bf16_ts(od, pd + kk * 8, dv + kk * 128, idesc_pv, (rp > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < steps; ++kk)
+              mma_bf16_ts(od, pd + kk * 8, dv + kk * 128, idesc_pv, (rp > 0 || kk > 0) ? 1u : 0u);
+          }
           mma_commit(&bars.v_empty[ip % VS]);
           mma_commit(&bars.pv_done[ip & 1]);
           ++ip;
@@ -568,7 +575,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           fence_after();
           const uint64_t dq = smem_desc(base + Sh::kQ, 16, 1024), dk = smem_desc(base + Sh::kK + (is % KS) * TB, 16, 1024);
           const uint32_t sd = tmem + kColS + (is % kSB) * 128;
-#pragma unroll 1
+#pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {           // (16 columns are 32 B, 64 a half tile)
             const uint32_t o = (kk >> 2) * (kHalfBytes >> 4) + (kk & 3) * 2;
             mma_bf16(sd, dq + o, dk + o, idesc_qk, kk > 0);
