@@ -411,9 +411,10 @@ TV_API tv_status tree_commit_kv(const tv_commit_args* a, tv_stream_t stream);
  * K/V values of tree nodes that are not on a node's root path do not reach
  * its rows, whatever they hold.
  * dtype TV_FP32 or TV_BF16, d in {32, 64, 128}, Hq / Hkv <= 64,
- * 1 <= page_size <= 65536, and fewer than 2^31 tiles of 64 keys over all
- * sequences, kv heads and row tiles, full tables counted; other values
- * TV_ERR_UNSUPPORTED.  out may not overlap the inputs.  Two launches; the split of the work over the GPU
+ * 1 <= page_size <= 65536, and fewer than 2^31 tiles of 64 keys (and one
+ * more a sequence, head and row tile) over all sequences, kv heads and row
+ * tiles, full tables counted; other values TV_ERR_UNSUPPORTED.  out may not
+ * overlap the inputs.  Two launches; the split of the work over the GPU
  * follows the lengths on the device, so max_pages costs nothing.
  * ---------------------------------------------------------------------- */
 typedef struct {

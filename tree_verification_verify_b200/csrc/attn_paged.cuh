@@ -6,7 +6,10 @@
 // rows); its key tiles are the prefix tiles of its sequence, then the tree
 // tiles.  All units' key tiles lie in one line, sequence by sequence, and
 // each CTA of a grid of about one CTA per SM takes an equal stretch of it:
-// a piece of a unit at either end, whole units between.  (Where sequences
+// a piece of a unit at either end, whole units between.  Behind its tiles a
+// unit has COST more places with nothing in them, as many as tiles could run
+// in the time that a kernel loses at the border of units (where a stretch is
+// four tiles or longer; shorter ones hold hardly more than a unit's piece).  (Where sequences
 // have several row tiles on the tensor cores, a team of CTAs takes a stretch
 // together, a row tile each, so that they read the same keys at the same
 // time and all but one find them in the L2.)  The line's length
@@ -64,7 +67,7 @@ struct SeqInfo {
   bool bad_len;
   int nprefix, ntree;          // key tiles of a unit
   int rem, off;                // the prefix's last rem rows share the one tree tile, whose nodes begin at row off
-  int len;                     // max(1, nprefix + ntree): a unit without keys still writes its rows
+  int tiles;                   // max(1, nprefix + ntree): a unit without keys still writes its rows
   int units;                   // row tiles * kv heads
 };
 
@@ -88,7 +91,7 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedAttnParams& p, int b, int
     s.rem = rem;
     s.off = off;
   }
-  s.len = max(1, s.nprefix + s.ntree);
+  s.tiles = max(1, s.nprefix + s.ntree);
   s.units = (s.n * p.G + p.rows - 1) / p.rows * p.Hkv;
   return s;
 }
@@ -97,54 +100,69 @@ constexpr int kMaxSlots = 512;
 
 // The line's prefix sums: slot t holds sequences [t * per, (t + 1) * per).
 struct Line {
-  int cum[kMaxSlots + 1];      // (the host refuses lines of 2^31 tiles)
-  int warp_sum[32];
+  int cum[kMaxSlots + 1];      // (the host refuses lines of 2^31 places)
+  int warp_sum[32], warp_units[32];
+  int cost;                    // places behind a unit's tiles
   int per;                     // sequences per slot
   int nslot;
   int first, last;             // this CTA's stretch
-  int step;                    // tiles of a stretch
+  int step;                    // places of a stretch
   int stretch;                 // this CTA's
 };
 
 // Called by all NT threads of the CTA (NT <= kMaxSlots, a multiple of 32).
-template <int KEYS, int NT>
+template <int KEYS, int COST, int NT>
 __device__ __forceinline__ void build_line(const PagedAttnParams& p, Line& ln, int align) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + NT - 1) / NT;
-  int v = 0;
+  int v = 0, u = 0;                                // tiles, units
+#pragma unroll 1
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b >= p.B) break;
     const SeqInfo s = seq_info<KEYS>(p, b, align);
-    v += s.units * s.len;
+    v += s.units * s.tiles;
+    u += s.units;
     if (blockIdx.x == 0 && p.n_nodes) {
       const int n = p.n_nodes[b];
       if (n < 0 || n > p.T) set_status(p.status, TV_DEV_BAD_LEN);
     }
     if (blockIdx.x == 0 && s.bad_len && s.n > 0) set_status(p.status, TV_DEV_BAD_LEN);
   }
-  int incl = v;
+  int incl = v, incl_u = u;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += t;
+    const int t = __shfl_up_sync(0xffffffffu, incl, o), tu = __shfl_up_sync(0xffffffffu, incl_u, o);
+    if (lane >= o) {
+      incl += t;
+      incl_u += tu;
+    }
   }
-  if (lane == 31) ln.warp_sum[warp] = incl;
+  if (lane == 31) {
+    ln.warp_sum[warp] = incl;
+    ln.warp_units[warp] = incl_u;
+  }
   __syncthreads();
-  int before = 0, total = 0;
+  int before = 0, total = 0, before_u = 0, units = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
-    const int t = ln.warp_sum[w];
+    const int t = ln.warp_sum[w], tu = ln.warp_units[w];
     before += w < warp ? t : 0;
+    before_u += w < warp ? tu : 0;
     total += t;
+    units += tu;
   }
-  ln.cum[tid] = before + incl - v;
+  const int stretches = static_cast<int>(gridDim.x) / p.team;
+  const int cost = total / 4 >= stretches ? COST : 0;
+  total += cost * units;
+  ln.cum[tid] = before + incl - v + cost * (before_u + incl_u - u);
   if (tid == 0) {
     ln.cum[NT] = total;
     ln.per = per;
     ln.nslot = NT;
-    const int n = static_cast<int>(gridDim.x) / p.team, c = static_cast<int>(blockIdx.x) / p.team;
-    const int step = max(1, (total + n - 1) / n);
+    ln.cost = cost;
+    const int c = static_cast<int>(blockIdx.x) / p.team;
+    const int step = max(1, (total + stretches - 1) / stretches);
     ln.step = step;
     ln.stretch = c;
     ln.first = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(step) * c));
@@ -159,14 +177,16 @@ __device__ __forceinline__ void build_line(const PagedAttnParams& p, Line& ln, i
 struct Piece {
   int b, g, rt;
   SeqInfo s;
-  int t0, t1;
-  int unit_first;              // the unit's place in the line
+  int t0, t1;                  // (t0 >= t1: only places behind the unit's tiles)
+  int next;                    // the place after the piece
+  int unit_first;              // the unit's first place
 };
 
 // The piece that begins at `pos` (ln.first <= pos < ln.last).
 template <int KEYS>
 __device__ __forceinline__ Piece piece_at(const PagedAttnParams& p, const Line& ln, int pos, int align) {
   int lo = 0, hi = min(ln.nslot, p.B);             // last slot whose sum is <= pos: the one that holds pos
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (ln.cum[mid] <= pos) lo = mid; else hi = mid;
@@ -174,17 +194,21 @@ __device__ __forceinline__ Piece piece_at(const PagedAttnParams& p, const Line& 
   Piece c;
   int base = ln.cum[lo];
   int b = lo * ln.per;
+#pragma unroll 1
   for (int i = 0; i < ln.per; ++i, ++b) {          // one step when B is at most the thread count
     c.s = seq_info<KEYS>(p, b, align);
-    const int w = c.s.units * c.s.len;
+    const int w = c.s.units * (c.s.tiles + ln.cost);
     if (pos < base + w) break;
     base += w;
   }
   c.b = b;
   const int off = pos - base;
-  const int u = off / c.s.len;
-  c.t0 = off - u * c.s.len;
-  c.t1 = min(c.s.len, c.t0 + ln.last - pos);
+  const int len = c.s.tiles + ln.cost;
+  const int u = off / len;
+  c.t0 = off - u * len;
+  const int places = min(len - c.t0, ln.last - pos);
+  c.t1 = min(c.s.tiles, c.t0 + places);
+  c.next = pos + places;
   const int nrt = c.s.units / p.Hkv;
   c.g = u / nrt;
   c.rt = u - c.g * nrt;
@@ -206,14 +230,26 @@ __device__ __forceinline__ int64_t lse_row(const PagedAttnParams& p, int b, int 
   return (static_cast<int64_t>(b) * p.T + packed / p.G) * p.Hq + g * p.G + packed % p.G;
 }
 
+// The stretch that holds the unit's last tile.
+__device__ __forceinline__ int last_stretch(const Line& ln, const Piece& c) {
+  return (c.unit_first + c.s.tiles - 1) / ln.step;
+}
+
 // The note of a piece that begins a unit and does not end it.
 __device__ __forceinline__ SplitUnit split_of(const Line& ln, const Piece& c, int packed0, int rows) {
-  return SplitUnit{(c.unit_first + c.s.len - 1) / ln.step, c.b, c.g, packed0, rows};
+  return SplitUnit{last_stretch(ln, c), c.b, c.g, packed0, rows};
 }
 
 constexpr float kLn2 = 0.6931471805599453f;
 
 }  // namespace paged
+
+// Places of the line behind a unit's tiles, at most.  On the tensor cores a
+// border costs 5 us, 3 to 4 tiles' time: with none, CTAs of one piece were
+// done after 185 us and those of ten after 234 (32 sequences of 16 to 64
+// nodes, prefixes up to 16384); the call takes 245 us so and 220 with 3.
+// CUDA cores: 255 us with 0, 248 with 1, 257 with 3 (16 sequences, fp32).
+constexpr int kPagedSimtCost = 1, kPagedTcCost = 3;
 
 cudaError_t launch_attn_paged_simt(const PagedAttnParams& p, int grid, cudaStream_t stream);
 // Combines the split units' rows.

@@ -75,12 +75,13 @@ attn_paged_simt_kernel(PagedAttnParams p, int vec) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wr = warp / WK, wk = warp % WK;
   const int G = p.G;
-  build_line<kKeys, kThreads>(p, ln, 0);
+  build_line<kKeys, kPagedSimtCost, kThreads>(p, ln, 0);
   SplitUnit split = {-1, 0, 0, 0, 0};
 
   for (int pos = ln.first; pos < ln.last;) {
     const Piece c = piece_at<kKeys>(p, ln, pos, 0);
-    pos += c.t1 - c.t0;
+    pos = c.next;
+    if (c.t0 >= c.t1) continue;
     const int n = c.s.n, L = c.s.L;
     const int packed0 = c.rt * R;
     const int rows = min(R, n * G - packed0);
@@ -258,7 +259,7 @@ attn_paged_simt_kernel(PagedAttnParams p, int vec) {
       }
       __syncthreads();
     }
-    const bool whole = c.t0 == 0 && c.t1 == c.s.len;
+    const bool whole = c.t0 == 0 && c.t1 == c.s.tiles;
     const int which = c.t0 == 0 ? 1 : 0;
     const int64_t slot0 = part_slot(p, blockIdx.x, which);
     // the WK warps of a row share its rows' output

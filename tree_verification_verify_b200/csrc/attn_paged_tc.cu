@@ -73,11 +73,12 @@ constexpr uint32_t kColS = 0, kColO = kSB * 128;
 constexpr uint16_t kRootMark = 0xFFFEu, kBadMark = 0xFFFFu;
 constexpr int kRing = 8, kAhead = 3;                      // descriptions kept, and made ahead
 
-// Shared memory: Q, the K and V rings (96 KB and 64 KB), two parent[] buffers.
+// Shared memory: Q, the K and V rings (64 KB and 96 KB: a V tile waits for the
+// softmax; the other way round took 6 % longer), two parent[] buffers.
 template <int D>
 struct Shape {
   static constexpr uint32_t kTile = D / 64 * kHalfBytes;  // bytes of a K, V or Q tile
-  static constexpr int kKS = 3 * 128 / D, kVS = 2 * 128 / D;
+  static constexpr int kKS = 2 * 128 / D, kVS = 3 * 128 / D;
   static constexpr uint32_t kQ = 0, kK = kTile, kV = kK + kKS * kTile, kPar = kV + kVS * kTile;
   static constexpr uint32_t kBytes = kPar + 2 * kMaxT * 2;
 };
@@ -100,7 +101,7 @@ struct Desc {
 
 struct Bars {
   uint64_t q_full, q_empty;
-  uint64_t k_full[6], k_empty[6], v_full[4], v_empty[4];
+  uint64_t k_full[4], k_empty[4], v_full[6], v_empty[6];
   uint64_t s_full[kSB], p_full[kSB];                      // S and P buffers
   uint64_t pv_done[2];                                    // P V, by tile parity
   uint64_t dec[4][2];                                     // [warp & 3][group] the group's rows have their reference maximum
@@ -166,6 +167,32 @@ __device__ __forceinline__ uint32_t mbar_test5(uint32_t b0, uint32_t b1, uint32_
   return r;
 }
 
+// Bounded wait on phase `parity`; false when the CTA aborted (nullptr: not
+// asked) or the limit expired (then the abort flag is raised).  Rolled, as
+// every loop here that can be: unrolled as the compiler would have it the
+// kernel has 144 KB of code, the warps' roles push one another out of the
+// instruction cache, and its speed changes by up to half with unrelated edits.
+__device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t parity, volatile int* abort, uint32_t limit = kWaitLimit) {
+  const uint32_t a = smem_u32(b);
+#pragma unroll 1
+  for (uint32_t it = 0; it < limit; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (abort != nullptr && (it & 255u) == 255u && *abort) return false;
+  }
+  if (abort != nullptr) *abort = 1;
+  return false;
+}
+// After an abort: work already issued completes.
+__device__ __forceinline__ void drain(uint64_t* b, uint32_t parity) { wait_for(b, parity, nullptr, kDrainLimit); }
+
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 // 16 consecutive columns of this thread's TMEM lane.
@@ -193,6 +220,27 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i]);
   tmem_st16u(taddr, u);
+}
+
+// Adds the values that are not finite, of the nodes that the row sees, to
+// the thread's columns of its row, which it has just written.
+template <int D>
+__device__ __forceinline__ void add_nonfinite(const PagedAttnParams& p, const Desc& d, int64_t slot, __nv_bfloat16* orow, int col,
+                                           int cols, int node, const uint16_t* par, bool whole) {
+  while (true) {
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.vt) + d.b * p.kt_sb + static_cast<int64_t>(node) * p.kt_st +
+                             static_cast<int64_t>(d.g) * p.kt_sh;
+#pragma unroll 1
+    for (int e = col; e < col + cols; ++e) {
+      const float x = __bfloat162float(v[e]);
+      if (fabsf(x) < INFINITY) continue;
+      if (whole) orow[e] = __float2bfloat16(__bfloat162float(orow[e]) + x);
+      else p.part_o[slot * D + e] += x;
+    }
+    const uint16_t up = par[node];
+    if (up >= kRootMark) break;
+    node = up;
+  }
 }
 
 }  // namespace ptc
@@ -250,7 +298,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
-  build_line<kKeys, kThreads>(p, ln, align);              // ends with a CTA barrier
+  build_line<kKeys, kPagedTcCost, kThreads>(p, ln, align);              // ends with a CTA barrier
   fence_after();
   const uint32_t tmem = bars.tmem_base;
 
@@ -258,7 +306,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   // wait ignores the abort flag: after an abort every role still walks the
   // pieces to the end, so that all rows are written)
   auto desc = [&](int k) -> const Desc* {
-    if (!mbar_wait_cluster(&bars.w_full[k % kRing], (k / kRing) & 1)) {
+    if (!wait_for(&bars.w_full[k % kRing], (k / kRing) & 1, nullptr)) {
       *abort = 1;
       return nullptr;
     }
@@ -299,7 +347,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       bool a = true;
       if (pending >= 0 && !__shfl_sync(0xffffffffu, lane == 0 ? mbar_test(&empty[s], ((it / NS) - 1) & 1) : false, 0))
         flush();
-      if (lane == 0) a = mbar_wait(&empty[s], ((it / NS) - 1) & 1, abort);
+      if (lane == 0) a = wait_for(&empty[s], ((it / NS) - 1) & 1, abort);
       return __all_sync(0xffffffffu, a);
     };
     for (int k = 0;; ++k) {
@@ -386,11 +434,12 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           }
           ok = acquire(s);
           if (!ok) break;
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < 4; ++i) {
+            const int64_t oi = i < 2 ? (i == 0 ? o[0] : o[1]) : (i == 2 ? o[2] : o[3]);
 #pragma unroll 4
             for (int r0 = 0; r0 < 32; r0 += RPI) {
-              const int64_t y = __shfl_sync(0xffffffffu, o[i], r0 + lane / CPR);
+              const int64_t y = __shfl_sync(0xffffffffu, oi, r0 + lane / CPR);
               const int rr = i * 32 + r0 + lane / CPR;
               if (y >= 0)
                 cp_async16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), ((y & 1) ? tree + (y - 1) : pool + y) + ch * 16);
@@ -410,7 +459,8 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     flush();
     // drain: every issued load lands before the CTA can exit
     if (lane == 0)
-      for (int j = (it > NS ? it - NS : 0); j < it; ++j) mbar_drain(&full[j % NS], (j / NS) & 1);
+#pragma unroll 1
+      for (int j = (it > NS ? it - NS : 0); j < it; ++j) drain(&full[j % NS], (j / NS) & 1);
     __syncwarp();
   } else if (warp == kWarpTree) {
     // ------------------------------------------------------------ pieces, Q and parent[]
@@ -420,15 +470,20 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       const int s = made % kRing;
       if (made >= kRing) {
         bool a = true;
-        if (lane == 0) a = mbar_wait_cluster(&bars.w_empty[s], ((made / kRing) - 1) & 1);
+        if (lane == 0) a = wait_for(&bars.w_empty[s], ((made / kRing) - 1) & 1, nullptr);
         if (!__all_sync(0xffffffffu, a)) { *abort = 1; more = false; return; }
       }
       Desc x;
-      x.valid = pos < ln.last;
+      Piece c;
+      x.valid = 0;
+#pragma unroll 1
+      while (!x.valid && pos < ln.last) {
+        c = piece_at<kKeys>(p, ln, pos, align);
+        pos = c.next;
+        x.valid = c.t0 < c.t1;
+      }
       more = x.valid;
       if (x.valid) {
-        const Piece c = piece_at<kKeys>(p, ln, pos, align);
-        pos += c.t1 - c.t0;
         x.unit_i0 = c.rt * npt * p.team;
         x.unit_nodes = min(npt * p.team, c.s.n - x.unit_i0);
         x.b = c.b; x.g = c.g; x.i0 = x.unit_i0 + member * npt;
@@ -449,9 +504,9 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         x.queue = queue;
         queue += x.cnt > 0;
         x.bad_len = c.s.bad_len;
-        x.whole = c.t0 == 0 && c.t1 == c.s.len;
+        x.whole = c.t0 == 0 && c.t1 == c.s.tiles;
         x.begins = c.t0 == 0;
-        x.c1 = (c.unit_first + c.s.len - 1) / ln.step;
+        x.c1 = last_stretch(ln, c);
       }
       if (lane == 0) {
         bars.desc[s] = x;
@@ -461,34 +516,31 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       ++made;
     };
     for (int k = 0;; ++k) {
+#pragma unroll 1
       while (more && made <= k + kAhead) make();
       if (k >= made) break;
       const Desc& d = bars.desc[k % kRing];               // (kept: this warp makes its successor in the ring)
       if (!d.valid) break;
       if (d.cnt == 0 || !ok) continue;
-      auto load_q = [&]() {
-        bool a = true;
-        if (nq > 0 && lane == 0) a = mbar_wait(&bars.q_empty, (nq - 1) & 1, abort);
-        ok = __all_sync(0xffffffffu, a);
-        if (!ok) return;
-        if (lane == 0) {
-          // rows past the tensor's nodes read as zeros
-          mbar_expect_tx(&bars.q_full, static_cast<uint32_t>(npt * G) * D * 2);
+      bool a = true;
+      if (nq > 0 && lane == 0) a = wait_for(&bars.q_empty, (nq - 1) & 1, abort);
+      ok = __all_sync(0xffffffffu, a);
+      if (!ok) continue;
+      if (lane == 0) {
+        // rows past the tensor's nodes read as zeros
+        mbar_expect_tx(&bars.q_full, static_cast<uint32_t>(npt * G) * D * 2);
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(&map_q, base + Sh::kQ + h * kHalfBytes, &bars.q_full, 64 * h, d.g * G, d.i0, d.b);
-        }
-        ++nq;
-      };
-      const bool first = nq == 0;
-      if (first) load_q();
-      if (ok && d.ntr > 0) {
+        for (int h = 0; h < D / 64; ++h)
+          tma_load_4d(&map_q, base + Sh::kQ + h * kHalfBytes, &bars.q_full, 64 * h, d.g * G, d.i0, d.b);
+      }
+      ++nq;
+      if (d.ntr > 0) {
         const int buf = ntree & 1;
-        bool a = true;
-        if (ntree >= 2 && lane == 0) a = mbar_wait(&bars.t_empty[buf], ((ntree >> 1) - 1) & 1, abort);
+        if (ntree >= 2 && lane == 0) a = wait_for(&bars.t_empty[buf], ((ntree >> 1) - 1) & 1, abort);
         ok = __all_sync(0xffffffffu, a);
         if (!ok) continue;
         const int32_t* par = p.parent + d.b * p.par_sb;
+#pragma unroll 1
         for (int j = lane; j < d.i0 + d.nodes; j += 32) {
           const int pj = par[j];
           spar[buf * kMaxT + j] = j == 0 ? (pj == -1 ? kRootMark : kBadMark)
@@ -498,9 +550,8 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (lane == 0) mbar_arrive(&bars.t_full[buf]);
         ++ntree;
       }
-      if (ok && !first) load_q();
     }
-    if (lane == 0 && nq > 0) mbar_drain(&bars.q_full, (nq - 1) & 1);
+    if (lane == 0 && nq > 0) drain(&bars.q_full, (nq - 1) & 1);
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
@@ -598,8 +649,11 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       }
       if (*abort) {
         // what was issued completes before the TMEM is freed
-        for (int j = is > kSB ? is - kSB : 0; j < is; ++j) mbar_drain(&bars.s_full[j % kSB], (j / kSB) & 1);
-        for (int j = ip > 2 ? ip - 2 : 0; j < ip; ++j) mbar_drain(&bars.pv_done[j & 1], (j >> 1) & 1);
+#pragma unroll 1
+        for (int j = is > kSB ? is - kSB : 0; j < is; ++j) drain(&bars.s_full[j % kSB], (j / kSB) & 1);
+#pragma unroll 1
+        for (int j = ip > 2 ? ip - 2 : 0; j < ip; ++j) drain(&bars.pv_done[j & 1], (j >> 1) & 1);
+#pragma unroll 1
         while (dp) next_p();
       }
     }
@@ -648,9 +702,10 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         if (tree) {
           if (cur == -2) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.t_full[ntree & 1], (ntree >> 1) & 1, abort));
+            ok = ok && __all_sync(0xffffffffu, wait_for(&bars.t_full[ntree & 1], (ntree >> 1) & 1, abort));
             cur = row_valid && ok ? my_node : -1;
           }
+#pragma unroll 1
           while (cur >= lo) {
             const int x = cur - lo + off;
 #pragma unroll
@@ -660,7 +715,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             cur = up >= kRootMark ? -1 : static_cast<int>(up);
           }
         }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.s_full[sb], (it / kSB) & 1, abort));
+        ok = ok && __all_sync(0xffffffffu, wait_for(&bars.s_full[sb], (it / kSB) & 1, abort));
         fence_after();
         if (live && ok) {
           float s[128];
@@ -680,14 +735,14 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           // the row's reference maximum after the tile before
           float m = -INFINITY;
           if (r > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars.dec[warp & 3][half ^ 1], ((it - 1) >> 1) & 1, abort));
+            ok = __all_sync(0xffffffffu, wait_for(&bars.dec[warp & 3][half ^ 1], ((it - 1) >> 1) & 1, abort));
             m = bars.m_ref[row];
           }
           const float m_new = fmaxf(m, mt);
           const bool grow = m_new > m + 8.0f;             // also the first finite maximum
           if (__any_sync(0xffffffffu, grow) && r > 0 && ok) {
             // O holds the tiles before this one: wait for the last P V, then rescale
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort));
+            ok = __all_sync(0xffffffffu, wait_for(&bars.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort));
             fence_after();
             const float factor = grow ? ex2_approx(m - m_new) : 1.f;   // 0 when m = -inf
 #pragma unroll 1
@@ -734,7 +789,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         if (!full) {
           // V rows of the K steps that are no keys are cleared, nodes' rows looked over
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.v_full[it % VS], (it / VS) & 1, abort));
+          ok = ok && __all_sync(0xffffffffu, wait_for(&bars.v_full[it % VS], (it / VS) & 1, abort));
           uint8_t* v0 = gbase + Sh::kV + (it % VS) * TB;
           uint32_t* vbad = bars.vbad[half][nfix & 3];
           auto chunk = [&](int x, int ch) {
@@ -743,11 +798,13 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           constexpr int CPR = D / 8;
           if (ok) {
             const int top = (end + 15) & ~15;
+#pragma unroll 1
             for (int e = tid & 127; e < (top - np) * CPR; e += 128) {
               const int x = np + e / CPR;
               if (!tree || x < off || x >= end) *chunk(x, e % CPR) = make_uint4(0u, 0u, 0u, 0u);
             }
             if (tree) {
+#pragma unroll 1
               for (int e = tid & 127; e < (end - off) * CPR; e += 128) {
                 const int x = off + e / CPR;
                 uint4* at = chunk(x, e % CPR);
@@ -784,7 +841,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       }
       // ---------------------------------------------------------- output
       it0 += cnt;
-      if (cnt > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.o_full, nout & 1, abort));
+      if (cnt > 0) ok = ok && __all_sync(0xffffffffu, wait_for(&bars.o_full, nout & 1, abort));
       // the groups' sums meet at the larger of their maxima, O's reference:
       // out = O / (2^(m_0 - M) l_0 + 2^(m_1 - M) l_1); group h writes half of the columns
       bars.red_m[half][row] = m_run;
@@ -820,22 +877,6 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             v0[e] = bad ? NAN : (empty ? 0.f : v0[e] * inv);
-          if (nf) {
-            // the values that are not finite, of the nodes this row sees
-            int j = my_node;
-            while (true) {
-              const __nv_bfloat16* vs = static_cast<const __nv_bfloat16*>(p.vt) + d->b * p.kt_sb +
-                                        static_cast<int64_t>(j) * p.kt_st + static_cast<int64_t>(d->g) * p.kt_sh + col;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float x = __bfloat162float(vs[e]);
-                if (!(fabsf(x) < INFINITY)) v0[e] += x;
-              }
-              const uint16_t up = par[j];
-              if (up >= kRootMark) break;
-              j = up;
-            }
-          }
           if (whole) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -853,6 +894,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                   make_float4(v0[4 * e], v0[4 * e + 1], v0[4 * e + 2], v0[4 * e + 3]);
           }
         }
+        if (nf && row_valid) add_nonfinite<D>(p, *d, slot, orow, half * NC, NC, my_node, par, whole);
         if (half == 0 && row_valid) {
           const float lse2 = bad ? NAN : (empty ? -INFINITY : M + log2f(l_row));
           if (!whole) p.part_lse[slot] = lse2;

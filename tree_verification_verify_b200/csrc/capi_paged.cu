@@ -76,7 +76,7 @@ tv_status check_attn_paged(const tv_attn_paged_args* a) {
 struct PagedPlan {
   bool tc;
   int rows, team, grid;        // grid: stretches times team
-  bool fits;                   // the line has fewer than 2^31 key tiles
+  bool fits;                   // the line has fewer than 2^31 places
   size_t off_o, off_lse, off_splits, total;
 };
 
@@ -91,7 +91,7 @@ PagedPlan plan_attn_paged(const tv_attn_paged_args* a) {
   const int64_t rt = (static_cast<int64_t>(a->T) * G + pl.rows - 1) / pl.rows;
   const int64_t tiles = (static_cast<int64_t>(a->max_pages) * a->page_size + keys - 1) / keys + (a->T + keys - 1) / keys;
   const int64_t most = static_cast<int64_t>(a->B) * a->Hkv * rt * (tiles > 0 ? tiles : 1);
-  pl.fits = most < (1ll << 31);
+  pl.fits = most + static_cast<int64_t>(a->B) * a->Hkv * rt * (pl.tc ? kPagedTcCost : kPagedSimtCost) < (1ll << 31);
   const int64_t want = static_cast<int64_t>(num_sms()) * (pl.tc ? 1 : attn_paged_simt_ctas(pl.rows, a->d));
   const int64_t stretches = std::max<int64_t>(1, std::min(most, want / pl.team));
   pl.grid = static_cast<int>(stretches * pl.team);
