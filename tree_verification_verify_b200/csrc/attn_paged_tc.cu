@@ -49,6 +49,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+
 #include "attn.cuh"
 #include "attn_paged.cuh"
 #include "tc_prims.cuh"
@@ -345,6 +347,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     auto acquire = [&](int s) -> bool {                   // the stage is free
       if (it < NS) return true;
       bool a = true;
+      // (no stage yet: the last tile is announced now instead of after the next one's copies)
       if (pending >= 0 && !__shfl_sync(0xffffffffu, lane == 0 ? mbar_test(&empty[s], ((it / NS) - 1) & 1) : false, 0))
         flush();
       if (lane == 0) a = wait_for(&empty[s], ((it / NS) - 1) & 1, abort);
@@ -409,40 +412,59 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       } else {
         const char* pool = static_cast<const char*>(isk ? p.kp : p.vp) + g * p.kv_sh * 2;
         const char* tree = static_cast<const char*>(isk ? p.kt : p.vt) + (b * p.kt_sb + g * p.kt_sh) * 2;
+        // pages of rows l, l + 32, ... of the next tile, read a tile ahead
+        int pg[4];
+        auto look = [&](int t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const unsigned pos = static_cast<unsigned>(t) * kKeys + i * 32 + lane;
+            pg[i] = pos < static_cast<unsigned>(L) ? __ldg(table + pos / P) : 0;
+          }
+        };
+        look(a0);
         for (int r = 0; ok && r < cnt; ++r, ++it) {
-          // lane l looks up rows l, l + 32, l + 64, l + 96: the byte offset in
-          // its source and, in bit 0, which source; -2: no row
+          // lane l looks up rows l, l + 32, l + 64, l + 96: the offset in its
+          // source in units of 16 bytes, the top bit for the tree; all ones: no row
           const int t = a0 + r, lo = lo0 - (t - a1) * kKeys;
           const int np = t < a1 ? kKeys : rem;            // prefix rows (as far as the prefix goes)
           const int s = it % NS;
           constexpr int CPR = D / 8, RPI = 32 / CPR;      // 16-byte chunks of a row, rows of a step
+          constexpr uint32_t kTree = 0x80000000u, kNone = 0xffffffffu;
           const int ch = lane % CPR;
-          const uint32_t dst = ring + s * TB + ch / 8 * kHalfBytes;
-          int64_t o[4];
+          uint32_t o[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int x = i * 32 + lane;
-            o[i] = -2;
+            o[i] = kNone;
             const unsigned pos = static_cast<unsigned>(t) * kKeys + x;
             if (x < np && pos < static_cast<unsigned>(L)) {
-              const int page = __ldg(table + pos / P);
-              if (page < 0 || page >= p.num_pages) bad_page();
-              else o[i] = (page * p.kv_sp + static_cast<int64_t>(pos % P) * p.kv_sr) * 2;
+              if (pg[i] < 0 || pg[i] >= p.num_pages) bad_page();
+              else o[i] = static_cast<uint32_t>((pg[i] * p.kv_sp + static_cast<int64_t>(pos % P) * p.kv_sr) / 8);
             } else if (t >= a1 && x >= off && lo + x - off < nodes) {
-              o[i] = static_cast<int64_t>(lo + x - off) * p.kt_st * 2 + 1;
+              o[i] = static_cast<uint32_t>(static_cast<int64_t>(lo + x - off) * p.kt_st / 8) | kTree;
             }
           }
+          if (r + 1 < cnt) look(t + 1);
           ok = acquire(s);
           if (!ok) break;
+          // (one warp issues 2048 copies a tile: what it does for each counts.
+          // With 64-bit offsets, the swizzle worked out each time and the
+          // pages read when they are needed: 838 us for 64 sequences' decode
+          // over pages of 5 rows, so 430; pages of 16 rows take 200)
+          uint32_t at[8 / RPI];                           // the chunk's place in rows r0 + lane / CPR, r0 = 0, RPI, ... 8 - RPI
+#pragma unroll
+          for (int i = 0; i < 8 / RPI; ++i) {
+            const int rr = i * RPI + lane / CPR;
+            at[i] = ring + s * TB + ch / 8 * kHalfBytes + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+          }
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
-            const int64_t oi = i < 2 ? (i == 0 ? o[0] : o[1]) : (i == 2 ? o[2] : o[3]);
-#pragma unroll 4
+            const uint32_t oi = i < 2 ? (i == 0 ? o[0] : o[1]) : (i == 2 ? o[2] : o[3]);
+#pragma unroll
             for (int r0 = 0; r0 < 32; r0 += RPI) {
-              const int64_t y = __shfl_sync(0xffffffffu, oi, r0 + lane / CPR);
-              const int rr = i * 32 + r0 + lane / CPR;
-              if (y >= 0)
-                cp_async16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), ((y & 1) ? tree + (y - 1) : pool + y) + ch * 16);
+              const uint32_t y = __shfl_sync(0xffffffffu, oi, r0 + lane / CPR);
+              const char* src = (y & kTree ? tree : pool) + static_cast<uint64_t>(y & ~kTree) * 16;
+              if (y != kNone) cp_async16(at[r0 / RPI % (8 / RPI)] + (i * 32 + r0 / 8 * 8) * 128, src + ch * 16);
             }
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
@@ -973,6 +995,12 @@ bool attn_paged_tc_supported(const tv_attn_paged_args* a) {
   if (!stride_ok(a->Hkv, a->kv_sh) || !stride_ok(a->page_size, a->kv_sr) || !stride_ok(a->num_pages, a->kv_sp)) return false;
   if (!stride_ok(a->Hkv, a->kt_sh) || !stride_ok(a->T, a->kt_st) || !stride_ok(a->B, a->kt_sb)) return false;
   if (!stride_ok(a->Hq, a->o_sh) || !stride_ok(a->T, a->o_st) || !stride_ok(a->B, a->o_sb)) return false;
+  // row by row, a row's place in its pool is 31 bits of 16-byte units
+  constexpr int64_t kMost = 1ll << 34;
+  const int64_t page = std::max(stride_or(a->num_pages, a->kv_sp), stride_or(a->page_size, a->kv_sr) * a->page_size);
+  if (attn_paged_tc_box(a->page_size) == 0 &&
+      (page >= kMost / a->num_pages || stride_or(a->T, a->kt_st) >= kMost / a->T))
+    return false;
   const uintptr_t al = reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(a->k_pages) |
                        reinterpret_cast<uintptr_t>(a->v_pages) | reinterpret_cast<uintptr_t>(a->k_tree) |
                        reinterpret_cast<uintptr_t>(a->v_tree) | reinterpret_cast<uintptr_t>(a->out);
