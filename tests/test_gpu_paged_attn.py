@@ -74,6 +74,37 @@ def test_a_long_sequence_is_split_over_the_gpu_and_merged(dtype):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+# more rows than one row tile: two, three and seven tiles of 128 rows, read by
+# teams of two and four; trees of several key tiles; sequences of few nodes
+# next to those of many
+TEAMS = [
+    (2, 40, 16, 2, 128, 16, [600, 77], "random", [40, 17]),
+    (3, 200, 8, 2, 64, 16, [700, 0, 129], "random", [200, 3, 130]),
+    (2, 50, 12, 2, 128, 32, [300, 1], "bfs", [43, 42]),
+    (2, 600, 2, 2, 128, 64, [40, 200], "random", [600, 513]),
+    (1, 150, 20, 4, 128, 5, [333], "bfs", None),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("s", TEAMS, ids=lambda s: "-".join(str(x) for x in s[:6]))
+def test_row_tiles_of_wide_trees(s, dtype):
+    B, T, Hq, Hkv, d, P, lens, tree, nn = s
+    _check(AttnCase(B, T, Hq, Hkv, d, P, lens, dtype, tree=tree, n_nodes=nn, seed=T + d))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 64)])
+@pytest.mark.parametrize("prefix_only", [False, True])
+def test_many_sequences_of_any_length(dtype, d, prefix_only):
+    """More tiles than four per CTA, so that borders of units count in the split; empty sequences among them."""
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(1, 5000, 24)]
+    lens[3] = lens[4] = lens[23] = 0
+    nn = [int(x) for x in rng.integers(0, 3, 24)]
+    c = AttnCase(24, 2, 8, 8, d, 16, lens, dtype, tree="chain", n_nodes=nn)
+    _check(c, prefix_only=prefix_only)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("layout", ["nphd", "nhpd"])
 def test_strided_pools_and_outputs(dtype, layout):

@@ -83,6 +83,26 @@ def test_accept_parity(mode, B, T, V, tree):
     _accept_check(*case, nn=nn)
 
 
+@pytest.mark.parametrize("mode", ["specsample", "specexec"])
+@pytest.mark.parametrize("B,T,V,tree", [(1, 3, 500001, "star"), (200, 3, 40000, "star"), (1, 4096, 300, "random")])
+def test_accept_rows_that_shared_memory_does_not_hold(mode, B, T, V, tree):
+    """Rows in pieces: a large vocabulary, many sequences (one CTA each), a tree that fills shared memory."""
+    if T > 1000:                                             # (a random tree's nodes have few children)
+        g = torch.Generator().manual_seed(9)
+        p, q, _ = _probs(B, T, V, 9)
+        par = trees(tree, B, T, 9)
+        tok = torch.randint(0, V, (B, T), generator=g).numpy()
+        if mode == "specexec":
+            for c in range(T):
+                kids = [j for j in range(1, T) if par[0, j] == c]
+                tok[0, kids] = np.random.default_rng(c).permutation(V)[:len(kids)]
+        u = torch.rand(2, B, T, generator=g, dtype=torch.float64)
+        case = p, (q if mode == "specsample" else None), tok, par, u[0], u[1]
+    else:
+        case = _accept_case(B, T, V, mode, tree, seed=B + T)
+    _accept_check(*case)
+
+
 def test_accept_many_rejections():
     """A star of drafts from an unrelated distribution: residual after residual at one node."""
     p, _, g = _probs(8, 30, 600, 3)
