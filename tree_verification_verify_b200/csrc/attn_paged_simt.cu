@@ -318,43 +318,48 @@ __global__ void __launch_bounds__(kThreads) attn_paged_merge_kernel(PagedAttnPar
 #endif
   const SplitUnit u = p.splits[c0];
   if (u.c1 < 0 || r >= u.rows) return;
-  // lane k: piece c0 + k's log-sum-exp (the first lies in the second slot of its CTA)
-  float M = -INFINITY;
+  // The pieces in order, U of them in flight (the first lies in the second
+  // slot of its stretch, the others in the first), under a running maximum.
+  constexpr int U = 16;
+  float M = -INFINITY, den = 0.f, acc[DL];
   bool bad = false;
-  for (int k = c0 + lane; k <= u.c1; k += 32) {
-    const float v = p.part_lse[part_slot(p, k, k == c0) + r];
-    bad |= v != v;
-    M = fmaxf(M, v);
-  }
-  bad = __any_sync(0xffffffffu, bad);
-  M = warp_max(M);
-  float acc[DL], den = 0.f;
 #pragma unroll
   for (int e = 0; e < DL; ++e) acc[e] = 0.f;
-  if (!bad && M > -INFINITY) {
-    constexpr int U = 8;                                   // pieces in flight
-    for (int k0 = c0; k0 <= u.c1; k0 += U) {
-      float o[U][DL], v[U];
+  for (int k0 = c0; k0 <= u.c1; k0 += U) {
+    float o[U][DL], v[U];
+    float m = M;
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int k = min(k0 + i, u.c1);
-        const int64_t s = part_slot(p, k, k == c0) + r;
-        v[i] = p.part_lse[s];
-        const float* src = p.part_o + s * D + lane * DL;
-        if (DL == 4) *reinterpret_cast<float4*>(o[i]) = *reinterpret_cast<const float4*>(src);
-        else if (DL == 2) *reinterpret_cast<float2*>(o[i]) = *reinterpret_cast<const float2*>(src);
-        else o[i][0] = src[0];
-      }
+    for (int i = 0; i < U; ++i) {
+      if (k0 + i > u.c1) break;
+      const int64_t s = part_slot(p, k0 + i, k0 + i == c0) + r;
+      v[i] = p.part_lse[s];
+      const float* src = p.part_o + s * D + lane * DL;
+      if (DL == 4) *reinterpret_cast<float4*>(o[i]) = *reinterpret_cast<const float4*>(src);
+      else if (DL == 2) *reinterpret_cast<float2*>(o[i]) = *reinterpret_cast<const float2*>(src);
+      else o[i][0] = src[0];
+    }
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const float w = k0 + i <= u.c1 ? exp2f(v[i] - M) : 0.f;
-        den += w;
-        if (w != 0.f) {
+    for (int i = 0; i < U; ++i) {
+      if (k0 + i > u.c1) break;
+      bad |= v[i] != v[i];
+      m = fmaxf(m, v[i]);
+    }
+    if (m == -INFINITY) continue;                          // no keys so far
+    const float f = exp2f(M - m);
+    den *= f;
 #pragma unroll
-          for (int e = 0; e < DL; ++e) acc[e] = fmaf(w, o[i][e], acc[e]);
-        }
+    for (int e = 0; e < DL; ++e) acc[e] *= f;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (k0 + i > u.c1) break;
+      const float w = exp2f(v[i] - m);
+      den += w;
+      if (w != 0.f) {
+#pragma unroll
+        for (int e = 0; e < DL; ++e) acc[e] = fmaf(w, o[i][e], acc[e]);
       }
     }
+    M = m;
   }
   const float inv = bad ? NAN : (den > 0.f ? 1.f / den : 0.f);
   const int packed = u.packed0 + r;
