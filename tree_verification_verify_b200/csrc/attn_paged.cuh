@@ -8,8 +8,10 @@
 // each CTA of a grid of about one CTA per SM takes an equal stretch of it:
 // a piece of a unit at either end, whole units between.  Behind its tiles a
 // unit has COST more places with nothing in them, as many as tiles could run
-// in the time that a kernel loses at the border of units (where a stretch is
-// four tiles or longer; shorter ones hold hardly more than a unit's piece).  (Where sequences
+// in the time that a kernel loses at the border of units.  Where a stretch is
+// shorter than four tiles that is too coarse: there every unit begins a
+// stretch of its own, if the stretches suffice for that or do when they are
+// one tile longer (one sequence of 4096 rows and 64 nodes: 33 us, so 28).  (Where sequences
 // have several row tiles on the tensor cores, a team of CTAs takes a stretch
 // together, a row tile each, so that they read the same keys at the same
 // time and all but one find them in the L2.)  The line's length
@@ -96,13 +98,15 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedAttnParams& p, int b, int
   return s;
 }
 
+__device__ __forceinline__ int round_up(int x, int m) { return (x + m - 1) / m * m; }
+
 constexpr int kMaxSlots = 512;
 
 // The line's prefix sums: slot t holds sequences [t * per, (t + 1) * per).
 struct Line {
   int cum[kMaxSlots + 1];      // (the host refuses lines of 2^31 places)
   int warp_sum[32], warp_units[32];
-  int cost;                    // places behind a unit's tiles
+  int cost, pad;               // a unit has its tiles, rounded up to `pad`, and `cost` more places
   int per;                     // sequences per slot
   int nslot;
   int first, last;             // this CTA's stretch
@@ -110,11 +114,46 @@ struct Line {
   int stretch;                 // this CTA's
 };
 
+// Places of a unit.
+__device__ __forceinline__ int places(int tiles, const Line& ln) {
+  return (ln.pad == 1 ? tiles : round_up(tiles, ln.pad)) + ln.cost;
+}
+
 // Called by all NT threads of the CTA (NT <= kMaxSlots, a multiple of 32).
 template <int KEYS, int COST, int NT>
 __device__ __forceinline__ void build_line(const PagedAttnParams& p, Line& ln, int align) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + NT - 1) / NT;
+  const int stretches = static_cast<int>(gridDim.x) / p.team;
+  // exclusive sums over the threads, and the totals
+  int before, before_u, sum, sum_u;
+  auto scan = [&](int v, int u) {
+    int incl = v, incl_u = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o), tu = __shfl_up_sync(0xffffffffu, incl_u, o);
+      if (lane >= o) {
+        incl += t;
+        incl_u += tu;
+      }
+    }
+    if (lane == 31) {
+      ln.warp_sum[warp] = incl;
+      ln.warp_units[warp] = incl_u;
+    }
+    __syncthreads();
+    before = incl - v;
+    before_u = incl_u - u;
+    sum = sum_u = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      const int t = ln.warp_sum[w], tu = ln.warp_units[w];
+      before += w < warp ? t : 0;
+      before_u += w < warp ? tu : 0;
+      sum += t;
+      sum_u += tu;
+    }
+  };
   int v = 0, u = 0;                                // tiles, units
 #pragma unroll 1
   for (int i = 0; i < per; ++i) {
@@ -129,40 +168,42 @@ __device__ __forceinline__ void build_line(const PagedAttnParams& p, Line& ln, i
     }
     if (blockIdx.x == 0 && s.bad_len && s.n > 0) set_status(p.status, TV_DEV_BAD_LEN);
   }
-  int incl = v, incl_u = u;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, incl, o), tu = __shfl_up_sync(0xffffffffu, incl_u, o);
-    if (lane >= o) {
-      incl += t;
-      incl_u += tu;
+  scan(v, u);
+  const bool brief = sum / 4 < stretches;          // stretches of up to four tiles
+  const int cost = brief ? 0 : COST;
+  int cum = before + cost * before_u, total = sum + cost * sum_u, pad = 1;
+  if (brief && sum > stretches) {
+    const int step = 2 + (sum > 2 * stretches) + (sum > 3 * stretches);
+    v = u = 0;                                     // places with the units' tiles rounded up to step, to step + 1
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b >= p.B) break;
+      const SeqInfo s = seq_info<KEYS>(p, b, align);
+      v += s.units * round_up(s.tiles, step);
+      u += s.units * round_up(s.tiles, step + 1);
+    }
+    __syncthreads();                               // the sums have been read
+    scan(v, u);
+    if (sum <= step * stretches) {
+      cum = before;
+      total = sum;
+      pad = step;
+    } else if (sum_u <= (step + 1) * stretches) {
+      cum = before_u;
+      total = sum_u;
+      pad = step + 1;
     }
   }
-  if (lane == 31) {
-    ln.warp_sum[warp] = incl;
-    ln.warp_units[warp] = incl_u;
-  }
-  __syncthreads();
-  int before = 0, total = 0, before_u = 0, units = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    const int t = ln.warp_sum[w], tu = ln.warp_units[w];
-    before += w < warp ? t : 0;
-    before_u += w < warp ? tu : 0;
-    total += t;
-    units += tu;
-  }
-  const int stretches = static_cast<int>(gridDim.x) / p.team;
-  const int cost = total / 4 >= stretches ? COST : 0;
-  total += cost * units;
-  ln.cum[tid] = before + incl - v + cost * (before_u + incl_u - u);
+  ln.cum[tid] = cum;
   if (tid == 0) {
     ln.cum[NT] = total;
     ln.per = per;
     ln.nslot = NT;
     ln.cost = cost;
+    ln.pad = pad;
     const int c = static_cast<int>(blockIdx.x) / p.team;
-    const int step = max(1, (total + stretches - 1) / stretches);
+    const int step = pad > 1 ? pad : max(1, (total + stretches - 1) / stretches);
     ln.step = step;
     ln.stretch = c;
     ln.first = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(step) * c));
@@ -197,18 +238,18 @@ __device__ __forceinline__ Piece piece_at(const PagedAttnParams& p, const Line& 
 #pragma unroll 1
   for (int i = 0; i < ln.per; ++i, ++b) {          // one step when B is at most the thread count
     c.s = seq_info<KEYS>(p, b, align);
-    const int w = c.s.units * (c.s.tiles + ln.cost);
+    const int w = c.s.units * places(c.s.tiles, ln);
     if (pos < base + w) break;
     base += w;
   }
   c.b = b;
   const int off = pos - base;
-  const int len = c.s.tiles + ln.cost;
+  const int len = places(c.s.tiles, ln);
   const int u = off / len;
   c.t0 = off - u * len;
-  const int places = min(len - c.t0, ln.last - pos);
-  c.t1 = min(c.s.tiles, c.t0 + places);
-  c.next = pos + places;
+  const int left = min(len - c.t0, ln.last - pos);
+  c.t1 = min(c.s.tiles, c.t0 + left);
+  c.next = pos + left;
   const int nrt = c.s.units / p.Hkv;
   c.g = u / nrt;
   c.rt = u - c.g * nrt;

@@ -275,24 +275,29 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     const CUtensorMap* m = tid == 32 ? &map_q : (tid == 33 ? &map_k : (tid == 34 ? &map_v : (tid == 35 ? &map_kt : &map_vt)));
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
   }
-  if (tid == 0) {
-    mbar_init(&bars.q_full, 1); mbar_init(&bars.q_empty, 1);
-    for (int s = 0; s < KS; ++s) { mbar_init(&bars.k_full[s], 1); mbar_init(&bars.k_empty[s], 1); }
-    for (int s = 0; s < VS; ++s) { mbar_init(&bars.v_full[s], 1); mbar_init(&bars.v_empty[s], 1); }
-    for (int s = 0; s < kSB; ++s) { mbar_init(&bars.s_full[s], 1); mbar_init(&bars.p_full[s], 4); }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars.pv_done[s], 1);
-      for (int i = 0; i < 4; ++i) mbar_init(&bars.dec[i][s], 1);
-      mbar_init(&bars.t_full[s], 1); mbar_init(&bars.t_empty[s], 8);
-      for (int i = 0; i < 16; ++i) bars.vbad[s][i >> 2][i & 3] = 0;
+  // (three threads share this while the first warps wait for the lengths)
+  if (lane == 0 && (warp == kWarpK || warp == kWarpV || warp == kWarpTree)) {
+    if (warp == kWarpK) {
+      for (int s = 0; s < KS; ++s) { mbar_init(&bars.k_full[s], 1); mbar_init(&bars.k_empty[s], 1); }
+      for (int s = 0; s < VS; ++s) { mbar_init(&bars.v_full[s], 1); mbar_init(&bars.v_empty[s], 1); }
+      mbar_init(&bars.q_full, 1); mbar_init(&bars.q_empty, 1);
+      mbar_init(&bars.o_full, 1); mbar_init(&bars.o_free, 8);
+    } else if (warp == kWarpV) {
+      for (int s = 0; s < kSB; ++s) { mbar_init(&bars.s_full[s], 1); mbar_init(&bars.p_full[s], 4); }
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&bars.pv_done[s], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&bars.dec[i][s], 1);
+        mbar_init(&bars.t_full[s], 1); mbar_init(&bars.t_empty[s], 8);
+      }
+      bars.abort = 0;
+    } else {
+      for (int s = 0; s < kRing; ++s) { mbar_init(&bars.w_full[s], 1); mbar_init(&bars.w_empty[s], 11); }
     }
-    mbar_init(&bars.o_full, 1); mbar_init(&bars.o_free, 8);
-    for (int s = 0; s < kRing; ++s) { mbar_init(&bars.w_full[s], 1); mbar_init(&bars.w_empty[s], 11); }
-    for (int i = 0; i < 8; ++i) bars.bad_piece[i] = 0;
-    bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  if (tid < 32) bars.vbad[tid >> 4][tid >> 2 & 3][tid & 3] = 0;
+  if (tid < 8) bars.bad_piece[tid] = 0;
   if (warp == kWarpMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem_base)),
                  "r"(kTmemCols)
@@ -539,7 +544,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     };
     for (int k = 0;; ++k) {
 #pragma unroll 1
-      while (more && made <= k + kAhead) make();
+      while (more && made <= (k == 0 ? 0 : k + kAhead)) make();   // (the first piece's Q before its successors)
       if (k >= made) break;
       const Desc& d = bars.desc[k % kRing];               // (kept: this warp makes its successor in the ring)
       if (!d.valid) break;
