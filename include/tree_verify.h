@@ -512,8 +512,8 @@ TV_API tv_status tree_accept_probs(const tv_accept_probs_args* a, tv_stream_t st
  * overlap the pool, and no two sequences may commit into one page.
  * dtype TV_FP32 or TV_BF16, 1 <= d <= 1024, B <= 16384.
  * Faults: n outside [0, T-1], L negative or L + n + 1 > max_pages *
- * page_size -> TV_DEV_BAD_LEN; a path node outside [1, T) or a path that
- * does not increase -> TV_DEV_BAD_ROW; a page of the rows written outside
+ * page_size or > 2^31 - 1 -> TV_DEV_BAD_LEN; a path node outside [1, T) or
+ * a path that does not increase -> TV_DEV_BAD_ROW; a page of the rows written outside
  * [0, num_pages) -> TV_DEV_BAD_PAGE.  Such a sequence's pages are left as
  * they were and its prefix_len_out is L.
  * The workspace holds ticket counters (zeroed once, left zero by every

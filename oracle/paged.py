@@ -163,7 +163,7 @@ def tree_commit_kv_paged(k_pages, v_pages, page_table, prefix_len, k_tree, v_tre
     status = 0
     for b in range(B):
         n, Lb = int(n_acc[b]), int(L[b])
-        if n < 0 or n > T - 1 or Lb < 0 or Lb + n + 1 > table.shape[1] * P:
+        if n < 0 or n > T - 1 or Lb < 0 or Lb + n + 1 > min(table.shape[1] * P, 2 ** 31 - 1):
             status |= ST_BAD_LEN
             continue
         rows = [0] + [int(acc[b, r]) for r in range(n)]

@@ -249,6 +249,25 @@ def test_offsets_past_32_bits(dtype, d):
     check_attn(out, lse, ref)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_the_longest_prefix(dtype):
+    """2^31 - 1 rows, all of one page: q = 0 gives every key the weight 1, V = 1 the output 1.  A CTA's sums are
+    integers below 2^24, hence exact; the merge rounds each of at most 592 pieces a few times (2^-24 each)."""
+    import tree_verification_verify_b200 as tv
+    from paged_util import DT
+    P, d = 65536, 64
+    k = torch.randn(1, P, 1, d, generator=torch.Generator().manual_seed(1)).to(DT[dtype]).cuda()
+    v = torch.ones_like(k)
+    one = torch.ones(1, 1, 1, d, dtype=DT[dtype], device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    st = i32([0])
+    out, lse = tv.tree_verify_attn_paged(one * 0, k, v, torch.zeros(1, 32768, dtype=torch.int32, device="cuda"),
+                                         i32([2 ** 31 - 1]), one, one, i32([[-1]]), dev_status=st)
+    assert int(st.item()) == 0
+    assert (out.double() - 1).abs().max().item() <= 600 * 4 * 2.0 ** -24
+    assert abs(lse.double().item() - np.log(2.0 ** 31)) <= (600 * 4 + 64) * 2.0 ** -24
+
+
 def test_streams_and_graphs_have_scratch_of_their_own():
     """Two captured graphs replayed at the same time on two streams, with eager calls between."""
     import tree_verification_verify_b200 as tv

@@ -318,6 +318,22 @@ def test_commit_faults_leave_a_sequence_alone():
     assert int(st.item()) == ref["status"] == op.ST_BAD_LEN | op.ST_BAD_ROW | op.ST_BAD_PAGE
 
 
+def test_commit_at_the_longest_length():
+    """A length is an int32: 2^31 - 2 rows take one more, 2^31 - 1 take none."""
+    import tree_verification_verify_b200 as tv
+    P = 65536
+    k = torch.zeros(2, P, 1, 4, device="cuda")
+    v = torch.zeros_like(k)
+    table = torch.zeros(2, 32768, dtype=torch.int32, device="cuda")
+    table[1] = 1
+    tree = torch.ones(2, 1, 1, 4, device="cuda")
+    L, st = dev([2 ** 31 - 2, 2 ** 31 - 1]), dev([0])
+    tv.tree_commit_kv_paged(k, v, table, L, tree, tree, dev([0, 0]), dev([[-1], [-1]]), dev_status=st)
+    torch.cuda.synchronize()
+    assert L.tolist() == [2 ** 31 - 1] * 2 and int(st.item()) == op.ST_BAD_LEN
+    assert k[0, P - 2].eq(1).all() and float(k.sum()) == 4 and float(v.sum()) == 4
+
+
 # ------------------------------------------------------------------ page tables
 
 def _update(k, v, table, src, keep, grow, W, pinned=None):

@@ -84,7 +84,7 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedAttnParams& p, int b, int
   s.n = (n < 0 || n > p.T) ? 0 : n;
   s.bad_len = L < 0 || L > cap;
   s.L = s.bad_len ? 0 : L;
-  s.nprefix = (s.L + KEYS - 1) / KEYS;
+  s.nprefix = static_cast<int>((static_cast<unsigned>(s.L) + KEYS - 1) / KEYS);
   s.ntree = p.prefix_only ? 0 : (s.n + KEYS - 1) / KEYS;
   s.rem = s.off = 0;
   const int rem = s.L % KEYS, off = align > 0 ? (rem + align - 1) / align * align : 0;

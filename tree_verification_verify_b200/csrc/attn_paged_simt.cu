@@ -115,11 +115,11 @@ attn_paged_simt_kernel(PagedAttnParams p, int vec) {
     // where key k of tile t lies; tree tiles run from the last one down
     auto locate = [&](int t, int k) -> int64_t {
       if (t < c.s.nprefix) {
-        const int j = t * kKeys + k;
-        if (j >= L) return -1;
-        const int page = table[j / p.page_size];
+        const unsigned j = static_cast<unsigned>(t) * kKeys + k, P = p.page_size;
+        if (j >= static_cast<unsigned>(L)) return -1;
+        const int page = table[j / P];
         if (page < 0 || page >= p.num_pages) { s_bad = 1; return -1; }
-        return page * p.kv_sp + static_cast<int64_t>(j % p.page_size) * p.kv_sr + c.g * p.kv_sh;
+        return page * p.kv_sp + static_cast<int64_t>(j % P) * p.kv_sr + c.g * p.kv_sh;
       }
       const int j = (c.s.ntree - 1 - (t - c.s.nprefix)) * kKeys + k;
       return j < n ? c.b * p.kt_sb + static_cast<int64_t>(j) * p.kt_st + c.g * p.kt_sh : -1;

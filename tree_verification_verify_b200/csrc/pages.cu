@@ -938,7 +938,7 @@ cudaError_t launch_commit_paged(const tv_commit_paged_args* a, void* ws, cudaStr
   CommitPagedParams p;
   p.pool = make_pool(a);
   p.layers = a->layers; p.B = a->B; p.T = a->T; p.P = a->page_size; p.num_pages = a->num_pages;
-  p.cap = static_cast<int64_t>(a->max_pages) * a->page_size;
+  p.cap = std::min<int64_t>(static_cast<int64_t>(a->max_pages) * a->page_size, INT32_MAX);   // (a length is an int32)
   p.table = a->page_table; p.pt_sb = a->pt_sb;
   p.len = a->prefix_len;
   p.len_out = a->prefix_len_out;
