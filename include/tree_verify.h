@@ -396,7 +396,8 @@ TV_API tv_status tree_commit_kv(const tv_commit_args* a, tv_stream_t stream);
  * [B][max_pages] int32 with row stride pt_sb; entries that hold no row of a
  * sequence are never looked at and may have any value (the calls below
  * write -1).  A page may be shared by several sequences, and K/V rows past
- * a sequence's end may hold anything, NaN included.
+ * a sequence's end may hold anything, NaN included.  Every call refuses pages
+ * of 2^31 elements or more a layer (TV_ERR_UNSUPPORTED).
  * ---------------------------------------------------------------------- */
 
 /* ------------------------------------------------------------------------
@@ -567,7 +568,7 @@ TV_API tv_status tree_commit_kv_paged(const tv_commit_paged_args* a, void* ws, s
  * [B][max_pages] (po_sb), which may not overlap page_table; source, keep,
  * grow [B] int32; pinned [num_pages] int32 or NULL; n_free [1] or NULL.
  * Limits: dtype TV_FP32 or TV_BF16, d <= 1024, B <= 16384, num_pages <=
- * 2^24 (TV_ERR_UNSUPPORTED beyond).
+ * 2^24, B * max_pages < 2^31 (TV_ERR_UNSUPPORTED beyond).
  * Faults: source outside [-1, B_in) -> TV_DEV_BAD_ROW; keep or grow
  * negative, keep > max_pages_in * page_size or keep + grow > max_pages *
  * page_size -> TV_DEV_BAD_LEN; a kept page outside [0, num_pages) ->

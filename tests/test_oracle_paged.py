@@ -273,7 +273,9 @@ def test_commit_paged_refusals(tv, kw, want):
     (dict(), WORKSPACE), (dict(B=-1), INVALID), (dict(source=None), INVALID), (dict(page_table_out=None), INVALID),
     (dict(page_table_out=8192), INVALID), (dict(page_table_out=8192 + 4 * 7), INVALID), (dict(po_sb=3), INVALID),
     (dict(pt_sb=3), INVALID), (dict(num_pages=(1 << 24) + 1), UNSUPPORTED), (dict(B_in=16385), UNSUPPORTED),
-    (dict(k_pages=None), INVALID), (dict(layers=-1), INVALID)])
+    (dict(k_pages=None), INVALID), (dict(layers=-1), INVALID),
+    (dict(B=16384, max_pages=1 << 17, po_sb=1 << 17), UNSUPPORTED),
+    (dict(page_size=65536, Hkv=64, d=512), UNSUPPORTED), (dict(page_size=65535, Hkv=32, d=1024), WORKSPACE)])
 def test_pages_update_refusals(tv, kw, want):
     a = tv.paged.PagesUpdateArgs(dtype=0, layers=1, B_in=2, B=2, Hkv=2, d=64, num_pages=8, page_size=16, max_pages_in=4,
                                  max_pages=4, page_table=8192, pt_sb=4, page_table_out=16384, po_sb=4)

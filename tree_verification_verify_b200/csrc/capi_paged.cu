@@ -27,6 +27,7 @@ namespace {
 constexpr int kMaxPageSize = 65536;
 constexpr int kMaxPages = 1 << 24;
 constexpr int kMaxSeqs = 16384;
+constexpr int64_t kMost = 1ll << 31;             // elements of a page of a layer, entries of a new table
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -48,6 +49,7 @@ tv_status check_pool(int dtype, int Hkv, int d, int num_pages, int page_size) {
   if (dtype != TV_FP32 && dtype != TV_BF16) return TV_ERR_INVALID_ARG;
   if (Hkv <= 0 || d < 1 || num_pages < 0 || page_size < 1) return TV_ERR_INVALID_ARG;
   if (page_size > kMaxPageSize || num_pages > kMaxPages) return TV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(Hkv) * d > (kMost - 1) / page_size) return TV_ERR_UNSUPPORTED;
   return TV_OK;
 }
 
@@ -230,6 +232,7 @@ tv_status check_update(const tv_pages_update_args* a) {
   if (st != TV_OK) return st;
   if (a->B < 0 || a->B_in < 0 || a->layers < 0 || a->max_pages < 0 || a->max_pages_in < 0) return TV_ERR_INVALID_ARG;
   if (a->d > 1024 || a->B > kMaxSeqs || a->B_in > kMaxSeqs || a->layers > 65535) return TV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(a->B) * a->max_pages >= kMost) return TV_ERR_UNSUPPORTED;
   if (a->layers > 0 && a->num_pages > 0) {
     if (!a->k_pages || !a->v_pages) return TV_ERR_INVALID_ARG;
     if (!elt_aligned(a->dtype, {a->k_pages, a->v_pages})) return TV_ERR_INVALID_ARG;
