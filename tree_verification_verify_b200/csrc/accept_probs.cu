@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(Params P) {
     }
     return;
   }
+  if (C > 1) cl.barrier_arrive();                // peers' shared memory is written to once they all run
   const int32_t* par = P.par + b * P.par_sb;
   const int32_t* tok = P.tok + b * P.tok_sb;
   const float* prow0 = P.p + b * P.tp_sb;
@@ -166,6 +167,7 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(Params P) {
   }
   if (rank == 0) set_status(P.status, bits);
   __syncthreads();
+  if (C > 1) cl.barrier_wait();
 
   int pass = 0;
   const int gw = rank * kWarps + warp;
