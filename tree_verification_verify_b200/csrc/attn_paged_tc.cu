@@ -9,12 +9,23 @@
 // prefix's last rows and a small tree share one tile.  Loads, products and
 // softmax of consecutive tiles overlap across the borders of units.
 //
+// What bounds it.  A steady tile takes about 2450 cycles (1.4 us) against 1024
+// each of the tensor pipe and the exponentials: with up to 128 rows a sequence
+// that is HBM (one sequence of 262144 rows, 16 nodes of 8 heads: 195 us, 5.5
+// TB/s; 32 sequences of up to 16 nodes on 512 to 16384 rows: 222 us, 5.2
+// TB/s), with more rows what the L2 hands the SMs, about 7 TB/s (two
+// sequences of 65537 to 131072 rows, 64 nodes of 4 heads: 245 us, 840
+// TFLOP/s; without the softmax's arithmetic, 207).  Beside the tiles: 5 to 8
+// us from the start to the first product, 5 us a border between units, 6 us
+// for the second kernel; those are most of a small call (one token on 700
+// rows: 16.4 us).
+//
 // Warp roles (384 threads):
 //   warps 0-7  softmax and output: two warpgroups, a thread per query row
 //              (TMEM lane), that take the key tiles in turn, so that one
 //              group's exponentials run while the other waits for TMEM and
-//              barriers (both on halves of the same tile: 5000 cycles a
-//              tile, half of them waits).  Warps without a valid row skip
+//              barriers (both on halves of the same tile: twice the time
+//              a tile, half of it waits).  Warps without a valid row skip
 //              the arithmetic (decoding: G of 128 rows are real);
 //   warp 8     K tiles, warp 10 V tiles.  Page sizes that are multiples of
 //              8 rows: one TMA box per run of rows that both the page and
@@ -34,7 +45,7 @@
 // by more than 8 (P <= 2^8, exact in O / l) and then rescales O itself, once
 // P V of tile j - 1 is done.  (With an accumulator and a maximum per group
 // there is room for two S buffers only, and S of a group's next tile has to
-// wait for P V of its last one: 3900 cycles a tile with 128 rows.)  P is
+// wait for P V of its last one: 3900 cycles a tile with 128 rows when one accumulator took 3000.)  P is
 // rounded to bf16 for the product with V (the tensor cores' operand type);
 // sums use the unrounded fp32 weights.
 //
