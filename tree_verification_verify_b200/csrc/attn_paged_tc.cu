@@ -756,11 +756,30 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         ok = ok && __all_sync(0xffffffffu, wait_for(&bars.s_full[sb], (it / kSB) & 1, abort));
         fence_after();
         if (live && ok) {
+          // d = 64 masks S where it lies and reads it again for the weights, in
+          // loops, a quarter of the code: 256 sequences' single tokens on 400
+          // to 700 rows 208 us, so 170, the other shapes within 2 %.  With d =
+          // 128 the longer waits for TMEM cost what the code saves.
+          constexpr bool kAgain = D == 64;
+          if (kAgain && !full) {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t w = q < 2 ? (q == 0 ? mk[0] : mk[1]) : (q == 2 ? mk[2] : mk[3]);
+              float z[32];
+              tmem_ld32(scol + q * 32, z);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 32; ++x) z[x] = ((w >> x) & 1u) ? z[x] : -INFINITY;
+              tmem_st16(scol + q * 32, z);
+              tmem_st16(scol + q * 32 + 16, z + 16);
+            }
+            tmem_wait_st();
+          }
           float s[128];
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32(scol + q * 32, s + q * 32);
           tmem_wait_ld();
-          if (!full) {
+          if (!kAgain && !full) {
 #pragma unroll
             for (int x = 0; x < 128; ++x) s[x] = ((mk[x >> 5] >> (x & 31)) & 1u) ? s[x] : -INFINITY;
           }
@@ -806,18 +825,29 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           // p = 2^(s sl2 - m) as bf16 pairs over the first half of S
           float2 ps[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
           const float2 sl = make_float2(sl2, sl2), nm = make_float2(nmu, nmu);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          auto weigh = [&](int q, const float* z) {
             uint32_t pk[16];
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
-              float2 e = fma2(make_float2(s[q * 32 + x], s[q * 32 + x + 1]), sl, nm);
+              float2 e = fma2(make_float2(z[x], z[x + 1]), sl, nm);
               e.x = ex2_approx(e.x);
               e.y = ex2_approx(e.y);
               ps[(x >> 1) & 3] = add2(ps[(x >> 1) & 3], e);
               pk[x / 2] = pack_bf16(e.x, e.y);
             }
             tmem_st16u(scol + q * 16, pk);
+          };
+          if constexpr (kAgain) {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              float z[32];
+              tmem_ld32(scol + q * 32, z);
+              tmem_wait_ld();
+              weigh(q, z);
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) weigh(q, s + q * 32);
           }
           const float2 sum = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
           l_run += sum.x + sum.y;
