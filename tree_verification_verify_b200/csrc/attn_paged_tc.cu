@@ -37,7 +37,13 @@
 //              to three tiles ahead or O += P V (P read from TMEM), so
 //              neither waits for the other's operands;
 //   warp 11    the pieces' descriptions, several ahead of their use (finding
-//              one takes a search and four divisions), Q and parent[].
+//              one takes a search and four divisions), Q and parent[].  Pieces
+//              without a tile are not described; this warp writes their rows.
+//              Every described piece has a tile, so the roles are at most a few
+//              pieces apart and the ring of descriptions never holds one up
+//              (the MMA thread looks for the next S while it still owes P V
+//              and has not given the older descriptions back: eight pieces
+//              without a tile in a row would stop it for good).
 // TMEM: three S buffers and one accumulator O.  The groups share O, and so
 // they share each row's reference maximum m: P = 2^(s - m).  The group with
 // tile j takes m over from the group with tile j - 1 (a barrier per pair of
@@ -100,16 +106,13 @@ struct Shape {
 // tree tiles whose first nodes are lo0, lo0 - 128, ...
 struct Desc {
   int valid;                    // 0: there are no more pieces
-  int cnt;                      // na + ntr
-  int index, queue;             // pieces before it, and those of them with tiles
+  int cnt;                      // na + ntr (at least 1)
   int b, g, i0;                 // sequence, kv head, first node of this CTA's row tile
-  int nodes;                    // nodes of the row tile (0: none)
-  int unit_i0, unit_nodes;      // of the whole unit
+  int nodes;                    // nodes of the row tile
   int n, L;                     // the sequence's nodes and prefix rows
   int a0, na, ntr, lo0;
   int rem, off;                 // the tree tile's prefix rows, and where its nodes begin
   int bad_len, whole, begins;
-  int c1;                       // the CTA in which the unit ends
 };
 
 struct Bars {
@@ -256,6 +259,30 @@ __device__ __forceinline__ void add_nonfinite(const PagedAttnParams& p, const De
   }
 }
 
+// The rows of a piece that has no tile of the row tile's keys, by one warp: a
+// unit without keys, or tree tiles of later nodes alone.
+template <int D>
+__device__ __forceinline__ void write_no_keys(const PagedAttnParams& p, const Desc& d, int64_t slot) {
+  const int lane = threadIdx.x & 31;
+  const float x = d.bad_len ? NAN : 0.f, z = d.bad_len ? NAN : -INFINITY;
+  const uint32_t xx = pack_bf16(x, x);
+#pragma unroll 1
+  for (int e = lane; e < d.nodes * p.G * (D / 8); e += 32) {
+    const int r = e / (D / 8), col = e % (D / 8) * 8;
+    if (d.whole) {
+      *reinterpret_cast<uint4*>(out_row<__nv_bfloat16>(p, d.b, d.g, d.i0 * p.G + r) + col) = make_uint4(xx, xx, xx, xx);
+    } else {
+      float4* o = reinterpret_cast<float4*>(p.part_o + (slot + r) * D + col);
+      o[0] = o[1] = make_float4(x, x, x, x);
+    }
+  }
+#pragma unroll 1
+  for (int r = lane; r < d.nodes * p.G; r += 32) {
+    if (!d.whole) p.part_lse[slot + r] = z;
+    else if (p.lse) p.lse[lse_row(p, d.b, d.g, d.i0 * p.G + r)] = z;
+  }
+}
+
 }  // namespace ptc
 
 using namespace ptc;
@@ -374,8 +401,8 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       if (!d) break;
       const int32_t* table = p.table + d->b * p.pt_sb;
       const int L = d->L, g = d->g, b = d->b, a0 = d->a0, a1 = d->a0 + d->na, cnt = d->cnt;
-      const int rem = d->rem, off = d->off, nodes = d->n, lo0 = d->lo0, index = d->index;
-      auto bad_page = [&]() { if (isk) bars.bad_piece[index & 7] = index + 1; };
+      const int rem = d->rem, off = d->off, nodes = d->n, lo0 = d->lo0;
+      auto bad_page = [&]() { if (isk) bars.bad_piece[k & 7] = k + 1; };
       if (box > 0) {
         // lane l holds the run of `box` rows number l % nb of tile l / nb of
         // a batch of 32 / nb tiles; the tile after the last prefix tile may
@@ -502,8 +529,9 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     __syncwarp();
   } else if (warp == kWarpTree) {
     // ------------------------------------------------------------ pieces, Q and parent[]
-    int nq = 0, ntree = 0, made = 0, queue = 0, pos = ln.first;
+    int nq = 0, ntree = 0, made = 0, pos = ln.first;
     bool ok = true, more = true;
+    SplitUnit split = {-1, 0, 0, 0, 0};
     auto make = [&]() {                                   // description number `made`
       const int s = made % kRing;
       if (made >= kRing) {
@@ -512,40 +540,35 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (!__all_sync(0xffffffffu, a)) { *abort = 1; more = false; return; }
       }
       Desc x;
-      Piece c;
       x.valid = 0;
 #pragma unroll 1
       while (!x.valid && pos < ln.last) {
-        c = piece_at<kKeys>(p, ln, pos, align);
+        const Piece c = piece_at<kKeys>(p, ln, pos, align);
         pos = c.next;
-        x.valid = c.t0 < c.t1;
-      }
-      more = x.valid;
-      if (x.valid) {
-        x.unit_i0 = c.rt * npt * p.team;
-        x.unit_nodes = min(npt * p.team, c.s.n - x.unit_i0);
-        x.b = c.b; x.g = c.g; x.i0 = x.unit_i0 + member * npt;
-        x.nodes = max(0, min(npt, c.s.n - x.i0));
+        if (c.t0 >= c.t1) continue;
+        const int unit_i0 = c.rt * npt * p.team;
+        x.whole = c.t0 == 0 && c.t1 == c.s.tiles;
+        x.begins = c.t0 == 0;
+        if (x.begins && !x.whole) split = split_of(ln, c, unit_i0 * G, min(npt * p.team, c.s.n - unit_i0) * G);
+        x.b = c.b; x.g = c.g; x.i0 = unit_i0 + member * npt;
+        x.nodes = min(npt, c.s.n - x.i0);
+        if (x.nodes <= 0) continue;                       // a team mate's row tile is the last
         x.n = c.s.n; x.L = c.s.L;
+        x.bad_len = c.s.bad_len;
         x.a0 = min(c.t0, c.s.nprefix);
         x.na = min(c.t1, c.s.nprefix) - x.a0;
         // tree tiles of later nodes than the row tile's are left out
-        const int skip = c.s.ntree > 0 ? c.s.ntree - ((x.i0 + max(x.nodes, 1) - 1) / kKeys + 1) : 0;
+        const int skip = c.s.ntree > 0 ? c.s.ntree - ((x.i0 + x.nodes - 1) / kKeys + 1) : 0;
         const int b0 = max(c.t0, c.s.nprefix + skip), b1 = min(c.t1, c.s.nprefix + c.s.ntree);
         x.ntr = max(0, b1 - b0);
         x.lo0 = (c.s.ntree - 1 - (b0 - c.s.nprefix)) * kKeys;
         x.rem = x.ntr > 0 ? c.s.rem : 0;
         x.off = x.ntr > 0 ? c.s.off : 0;
-        if (x.nodes == 0) x.na = x.ntr = 0;               // a team mate's row tile is the last
         x.cnt = x.na + x.ntr;
-        x.index = made;
-        x.queue = queue;
-        queue += x.cnt > 0;
-        x.bad_len = c.s.bad_len;
-        x.whole = c.t0 == 0 && c.t1 == c.s.tiles;
-        x.begins = c.t0 == 0;
-        x.c1 = last_stretch(ln, c);
+        x.valid = x.cnt > 0;
+        if (!x.valid) write_no_keys<D>(p, x, part_slot(p, ln.stretch, x.begins) + member * npt * G);
       }
+      more = x.valid;
       if (lane == 0) {
         bars.desc[s] = x;
         mbar_arrive(&bars.w_full[s]);
@@ -559,7 +582,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       if (k >= made) break;
       const Desc& d = bars.desc[k % kRing];               // (kept: this warp makes its successor in the ring)
       if (!d.valid) break;
-      if (d.cnt == 0 || !ok) continue;
+      if (!ok) continue;
       bool a = true;
       if (nq > 0 && lane == 0) a = wait_for(&bars.q_empty, (nq - 1) & 1, abort);
       ok = __all_sync(0xffffffffu, a);
@@ -590,6 +613,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       }
     }
     if (lane == 0 && nq > 0) drain(&bars.q_full, (nq - 1) & 1);
+    if (lane == 0 && member == 0) p.splits[ln.stretch] = split;
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
@@ -600,24 +624,18 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       int rs = 0, rp = 0;                                 // of those, in the present pieces
       int ks = -1, kp = -1;                               // the present pieces
       const Desc *ds = nullptr, *dp = nullptr;
-      int cnt_s = 0, cnt_p = 0, queue_s = 0, queue_p = 0; // tiles of the present pieces, pieces before them
+      int cnt_s = 0, cnt_p = 0;                           // tiles of the present pieces
       int na = 0, keys0 = 0, nodes = 0, lo0 = 0, off = 0; // of the piece of the next P V
       auto next_s = [&]() {
-        do ds = desc(++ks); while (ds && ds->cnt == 0);
-        if (ds) {
-          cnt_s = ds->cnt;
-          queue_s = ds->queue;
-        }
+        ds = desc(++ks);
+        if (ds) cnt_s = ds->cnt;
         rs = 0;
       };
       auto next_p = [&]() {
-        do {
-          if (kp >= 0) release(kp);
-          dp = desc(++kp);
-        } while (dp && dp->cnt == 0);
+        if (kp >= 0) release(kp);
+        dp = desc(++kp);
         if (dp) {
           cnt_p = dp->cnt;
-          queue_p = dp->queue;
           na = dp->na; keys0 = dp->L - dp->a0 * kKeys; nodes = dp->n; lo0 = dp->lo0; off = dp->off;
         }
         rp = 0;
@@ -626,16 +644,16 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       next_p();
       uint32_t idle = 0;
       while (dp) {
-        const uint32_t par = static_cast<uint32_t>((is / KS) & 1) | static_cast<uint32_t>(queue_s & 1) << 1 |
+        const uint32_t par = static_cast<uint32_t>((is / KS) & 1) | static_cast<uint32_t>(ks & 1) << 1 |
                              static_cast<uint32_t>((ip / VS) & 1) << 2 | static_cast<uint32_t>((ip / kSB) & 1) << 3 |
-                             static_cast<uint32_t>((queue_p - 1) & 1) << 4;
+                             static_cast<uint32_t>((kp - 1) & 1) << 4;
         const uint32_t got = mbar_test5(smem_u32(&bars.k_full[is % KS]), smem_u32(&bars.q_full), smem_u32(&bars.v_full[ip % VS]),
                                         smem_u32(&bars.p_full[ip % kSB]), smem_u32(&bars.o_free), par);
         const bool want_s = ds && is < ip + kSB, want_p = ip < is;
         bool did = false;
         // O += P V: P is bf16 pairs over the first 64 columns of its S.  The
         // first product of a piece overwrites O, so the last piece's must have been read.
-        if (want_p && (got & 12u) == 12u && (rp > 0 || queue_p == 0 || (got & 16u))) {
+        if (want_p && (got & 12u) == 12u && (rp > 0 || kp == 0 || (got & 16u))) {
           fence_after();
           const uint64_t dv = smem_desc(base + Sh::kV + (ip % VS) * TB, kHalfBytes, 1024);
           const uint32_t od = tmem + kColO, pd = tmem + kColS + (ip % kSB) * 128;
@@ -704,8 +722,6 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t ocol = trow + kColO;
     int it0 = 0, ntree = 0, nfix = 0;                     // tiles, tree pieces, the group's tree tiles before this piece
-    int nout = 0;                                         // pieces with tiles before this one
-    SplitUnit split = {-1, 0, 0, 0, 0};
     bool ok = true;
     for (int k = 0;; ++k) {
       const Desc* d = desc(k);
@@ -909,7 +925,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       }
       // ---------------------------------------------------------- output
       it0 += cnt;
-      if (cnt > 0) ok = ok && __all_sync(0xffffffffu, wait_for(&bars.o_full, nout & 1, abort));
+      ok = ok && __all_sync(0xffffffffu, wait_for(&bars.o_full, k & 1, abort));
       // the groups' sums meet at the larger of their maxima, O's reference:
       // out = O / (2^(m_0 - M) l_0 + 2^(m_1 - M) l_1); group h writes half of the columns
       bars.red_m[half][row] = m_run;
@@ -926,7 +942,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       const float c_1 = (m_1 == -INFINITY) ? 0.f : ex2_approx(m_1 - M);
       // a group whose sum is NaN (a NaN score) makes the row NaN
       const float l_row = c_0 * l_0 + c_1 * l_1 + ((l_0 != l_0 || l_1 != l_1) ? NAN : 0.f);
-      const bool bad = d->bad_len || !my_ok || !ok || bars.bad_piece[d->index & 7] == d->index + 1;
+      const bool bad = d->bad_len || !my_ok || !ok || bars.bad_piece[k & 7] == k + 1;
       const bool empty = l_row == 0.f;
       const float inv = bad ? NAN : (empty ? 0.f : 1.f / l_row);
       const bool whole = d->whole;
@@ -973,24 +989,19 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       // O and parent[] are free for the pieces to come
       fence_before();
       __syncwarp();
-      if (cnt > 0) {
-        if (lane == 0) mbar_arrive(&bars.o_free);
-        ++nout;
-      }
+      if (lane == 0) mbar_arrive(&bars.o_free);
       if (d->ntr > 0) {
         if (lane == 0) mbar_arrive(&bars.t_empty[ntree & 1]);
         ++ntree;
       }
       if (tid == 0) {
-        if (bars.bad_piece[d->index & 7] == d->index + 1) set_status(p.status, TV_DEV_BAD_PAGE);
+        if (bars.bad_piece[k & 7] == k + 1) set_status(p.status, TV_DEV_BAD_PAGE);
         if (!ok) set_status(p.status, TV_DEV_TIMEOUT);
-        if (d->begins && !whole) split = SplitUnit{d->c1, d->b, d->g, d->unit_i0 * G, d->unit_nodes * G};
       }
       bar_sync(1, kSoftmaxThreads);                       // red_*, m_ref: read by all
       __syncwarp();
       if (lane == 0) release(k);
     }
-    if (tid == 0 && member == 0) p.splits[ln.stretch] = split;
   }
   fence_before();
   __syncthreads();
