@@ -685,6 +685,14 @@ TV_API tv_status tv_expand_exp(const double* t, double* out, int32_t n, tv_strea
  * polls = 0 restores normal waits.  Applies to the current device,
  * synchronously; not for use while expansion calls are in flight. */
 TV_API tv_status tv_expand_set_wait_limit(uint32_t polls);
+/* Test hook for the bounded waits of tree_verify_attn_paged on the tensor
+ * cores (path 1): in the calls that follow, every CTA behaves as if a wait had
+ * run out, the one that its pieces of work after the first depend on
+ * (lost = 1) or the one that its products depend on (lost = 2); nothing that
+ * was started is lost.  All rows that have keys come out as NaN, lse too, and
+ * TV_DEV_TIMEOUT is set in dev_status.  lost = 0 ends it.  Host only; a
+ * captured graph keeps what held at its capture. */
+TV_API tv_status tv_attn_paged_set_lost(int32_t lost);
 
 #ifdef __cplusplus
 }

@@ -49,6 +49,7 @@ struct PagedAttnParams {
   int rows;                    // query rows of a unit
   int team;                    // CTAs that share a stretch, each with one row tile of its units
   int box;                     // tensor cores: rows of a page that one TMA box takes (0: row by row)
+  int lost;                    // tensor cores, a test hook: 1 no piece after a CTA's first comes, 2 no product
   float* part_o;               // [stretch][2][rows][d]: the piece that continues a unit, the one that begins one
   float* part_lse;             // [stretch][2][rows], log2 units
   struct SplitUnit* splits;    // [stretch] the unit that begins in it and ends in a later one
@@ -299,7 +300,8 @@ bool attn_paged_tc_supported(const tv_attn_paged_args* a);
 // Row tiles of a unit of the tensor-core kernel (a CTA each), and its TMA boxes.
 int attn_paged_tc_team(const tv_attn_paged_args* a);
 int attn_paged_tc_box(int page_size);
-cudaError_t launch_attn_paged_tc(const PagedAttnParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_attn_paged_tc(PagedAttnParams& p, int grid, cudaStream_t stream);
+void attn_paged_set_lost(int lost);                        // tv_attn_paged_set_lost
 // Query rows of the CUDA-core kernel's row tile and its CTAs per SM.
 int attn_paged_simt_rows(int64_t rows);
 int attn_paged_simt_ctas(int rows, int d);

@@ -61,12 +61,21 @@
 // one adds those values to its output at the end (an infinity or a NaN takes
 // over whatever its weight).  Rows of the last K steps that are no keys are
 // cleared; later K steps are not issued.
-// Every mbarrier wait is bounded: on expiry the CTA records TV_DEV_TIMEOUT,
-// drains what it issued, frees its TMEM, and its rows come out as NaN.
+// Every mbarrier wait is bounded (a failing poll takes 3.2 us, the limit 13 s).
+// On expiry the flag `going` falls, which the waits for tiles heed; the roles
+// drain what they issued and leave.  The softmax warps meet at block barriers
+// within a piece, so they may not leave at different pieces: they walk all
+// that warp 11 has described, and when it gives up it says which piece is the
+// first that will not be described.  When they are done warp 11 records
+// TV_DEV_TIMEOUT and writes NaN into all rows of the CTA's stretch, those that
+// were finished among them: nothing of an earlier call is left in the outputs
+// or in the partial rows.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
+#include <climits>
 
 #include "attn.cuh"
 #include "attn_paged.cuh"
@@ -91,6 +100,7 @@ constexpr int kSB = 3;                                    // S buffers, 128 colu
 constexpr uint32_t kColS = 0, kColO = kSB * 128;
 constexpr uint16_t kRootMark = 0xFFFEu, kBadMark = 0xFFFFu;
 constexpr int kRing = 8, kAhead = 3;                      // descriptions kept, and made ahead
+constexpr int kLostPieces = 1, kLostProducts = 2;         // PagedAttnParams::lost
 
 // Shared memory: Q, the K and V rings (64 KB and 96 KB: a V tile waits for the
 // softmax; the other way round took 6 % longer), two parent[] buffers.
@@ -125,7 +135,8 @@ struct Bars {
   uint64_t t_full[2], t_empty[2];                         // parent[] buffers
   uint64_t w_full[kRing], w_empty[kRing];                 // piece descriptions
   uint32_t tmem_base;
-  int abort;
+  int going;                                              // 0 after a wait that ran out
+  int end_at;                                             // the first piece that will not be described, once warp 11 gave up
   int bad_piece[8];                                       // piece number + 1 that met a bad page
   uint32_t vbad[2][4][4];                                 // [group][its tree tile & 3] V rows with infinities or NaN
   Desc desc[kRing];
@@ -183,12 +194,14 @@ __device__ __forceinline__ uint32_t mbar_test5(uint32_t b0, uint32_t b1, uint32_
   return r;
 }
 
-// Bounded wait on phase `parity`; false when the CTA aborted (nullptr: not
-// asked) or the limit expired (then the abort flag is raised).  Rolled, as
+// Bounded wait on phase `parity`; false when the CTA gives up (going nullptr:
+// not asked) or the limit expired (then the flag falls).  Rolled, as
 // every loop here that can be: unrolled as the compiler would have it the
 // kernel has 144 KB of code, the warps' roles push one another out of the
 // instruction cache, and its speed changes by up to half with unrelated edits.
-__device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t parity, volatile int* abort, uint32_t limit = kWaitLimit) {
+// (With the limit a parameter of the kernel, 64 sequences' single tokens took
+// 225 us for 200.)
+__device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t parity, volatile int* going, uint32_t limit = kWaitLimit) {
   const uint32_t a = smem_u32(b);
 #pragma unroll 1
   for (uint32_t it = 0; it < limit; ++it) {
@@ -201,14 +214,15 @@ __device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t parity, volatile 
         : "r"(a), "r"(parity)
         : "memory");
     if (ok) return true;
-    if (abort != nullptr && (it & 255u) == 255u && *abort) return false;
+    if (going != nullptr && (it & 255u) == 255u && *going <= 0) return false;
   }
-  if (abort != nullptr) *abort = 1;
+  if (going != nullptr) *going = 0;
   return false;
 }
-// After an abort: work already issued completes.
+// After giving up: work already issued completes.
 __device__ __forceinline__ void drain(uint64_t* b, uint32_t parity) { wait_for(b, parity, nullptr, kDrainLimit); }
 
+__device__ __forceinline__ void bar_arrive(int id, int n) { asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 // 16 consecutive columns of this thread's TMEM lane.
@@ -259,12 +273,12 @@ __device__ __forceinline__ void add_nonfinite(const PagedAttnParams& p, const De
   }
 }
 
-// The rows of a piece that has no tile of the row tile's keys, by one warp: a
-// unit without keys, or tree tiles of later nodes alone.
+// The rows of a piece by one warp, without keys (a unit that has none, or tree
+// tiles of later nodes alone) or as NaN.
 template <int D>
-__device__ __forceinline__ void write_no_keys(const PagedAttnParams& p, const Desc& d, int64_t slot) {
+__device__ __forceinline__ void fill_rows(const PagedAttnParams& p, const Desc& d, int64_t slot, bool nan) {
   const int lane = threadIdx.x & 31;
-  const float x = d.bad_len ? NAN : 0.f, z = d.bad_len ? NAN : -INFINITY;
+  const float x = nan ? NAN : 0.f, z = nan ? NAN : -INFINITY;
   const uint32_t xx = pack_bf16(x, x);
 #pragma unroll 1
   for (int e = lane; e < d.nodes * p.G * (D / 8); e += 32) {
@@ -307,7 +321,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   const uint32_t base = (raw + 1023u) & ~1023u;           // 128B swizzle atoms are 1 KB
   uint8_t* gbase = dsmem_raw + (base - raw);
   uint16_t* spar = reinterpret_cast<uint16_t*>(gbase + Sh::kPar);
-  volatile int* abort = &bars.abort;
+  volatile int* going = &bars.going;
 
   if (tid >= 32 && tid < 37) {
     const CUtensorMap* m = tid == 32 ? &map_q : (tid == 33 ? &map_k : (tid == 34 ? &map_v : (tid == 35 ? &map_kt : &map_vt)));
@@ -327,7 +341,8 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         for (int i = 0; i < 4; ++i) mbar_init(&bars.dec[i][s], 1);
         mbar_init(&bars.t_full[s], 1); mbar_init(&bars.t_empty[s], 8);
       }
-      bars.abort = 0;
+      bars.going = 1;
+      bars.end_at = INT_MAX;
     } else {
       for (int s = 0; s < kRing; ++s) { mbar_init(&bars.w_full[s], 1); mbar_init(&bars.w_empty[s], 11); }
     }
@@ -347,13 +362,26 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   fence_after();
   const uint32_t tmem = bars.tmem_base;
 
-  // Description k, and its release (every consuming warp once per piece; the
-  // wait ignores the abort flag: after an abort every role still walks the
-  // pieces to the end, so that all rows are written)
-  auto desc = [&](int k) -> const Desc* {
-    if (!wait_for(&bars.w_full[k % kRing], (k / kRing) & 1, nullptr)) {
-      *abort = 1;
-      return nullptr;
+  // Description k, and its release (every consuming warp once per piece);
+  // nullptr past the last one, and when it does not come.  Softmax warps
+  // ask whether it will: warp 11 describes it or says that it will not, after
+  // three waits of its own at most.  (All roles asking: 256 single tokens 190
+  // us for 182.)
+  auto desc = [&](int k, bool softmax) -> const Desc* {
+    uint64_t* w = &bars.w_full[k % kRing];
+    const uint32_t parity = (k / kRing) & 1;
+    if (!softmax) {
+      if (!wait_for(w, parity, nullptr)) {
+        *going = 0;
+        return nullptr;
+      }
+    } else {
+#pragma unroll 1
+      for (uint32_t n = 0; !wait_for(w, parity, nullptr, 1024); ++n)
+        if (n == kWaitLimit / 128 || *static_cast<volatile int*>(&bars.end_at) <= k) {
+          *going = 0;
+          return nullptr;
+        }
     }
     const Desc* d = &bars.desc[k % kRing];
     return d->valid ? d : nullptr;
@@ -393,12 +421,12 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       // (no stage yet: the last tile is announced now instead of after the next one's copies)
       if (pending >= 0 && !__shfl_sync(0xffffffffu, lane == 0 ? mbar_test(&empty[s], ((it / NS) - 1) & 1) : false, 0))
         flush();
-      if (lane == 0) a = wait_for(&empty[s], ((it / NS) - 1) & 1, abort);
+      if (lane == 0) a = wait_for(&empty[s], ((it / NS) - 1) & 1, going);
       return __all_sync(0xffffffffu, a);
     };
     for (int k = 0;; ++k) {
-      const Desc* d = desc(k);
-      if (!d) break;
+      const Desc* d = desc(k, false);
+      if (__any_sync(0xffffffffu, !d)) break;
       const int32_t* table = p.table + d->b * p.pt_sb;
       const int L = d->L, g = d->g, b = d->b, a0 = d->a0, a1 = d->a0 + d->na, cnt = d->cnt;
       const int rem = d->rem, off = d->off, nodes = d->n, lo0 = d->lo0;
@@ -530,14 +558,22 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   } else if (warp == kWarpTree) {
     // ------------------------------------------------------------ pieces, Q and parent[]
     int nq = 0, ntree = 0, made = 0, pos = ln.first;
-    bool ok = true, more = true;
+    bool ok = true, more = true, failed = false;
     SplitUnit split = {-1, 0, 0, 0, 0};
     auto make = [&]() {                                   // description number `made`
       const int s = made % kRing;
-      if (made >= kRing) {
+      if (made >= kRing || p.lost == kLostPieces) {
         bool a = true;
-        if (lane == 0) a = wait_for(&bars.w_empty[s], ((made / kRing) - 1) & 1, nullptr);
-        if (!__all_sync(0xffffffffu, a)) { *abort = 1; more = false; return; }
+        if (lane == 0) {
+          if (made >= kRing) a = wait_for(&bars.w_empty[s], ((made / kRing) - 1) & 1, going);
+          if (p.lost == kLostPieces && made > 0 && !failed) a = false;
+          if (!a) {
+            *going = 0;
+            *static_cast<volatile int*>(&bars.end_at) = made;
+          }
+        }
+        more = __all_sync(0xffffffffu, a);
+        if (!more) return;
       }
       Desc x;
       x.valid = 0;
@@ -565,10 +601,11 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         x.rem = x.ntr > 0 ? c.s.rem : 0;
         x.off = x.ntr > 0 ? c.s.off : 0;
         x.cnt = x.na + x.ntr;
-        x.valid = x.cnt > 0;
-        if (!x.valid) write_no_keys<D>(p, x, part_slot(p, ln.stretch, x.begins) + member * npt * G);
+        x.valid = x.cnt > 0 && !failed;
+        if (!x.valid) fill_rows<D>(p, x, part_slot(p, ln.stretch, x.begins) + member * npt * G, failed || x.bad_len);
       }
       more = x.valid;
+      if (failed) return;
       if (lane == 0) {
         bars.desc[s] = x;
         mbar_arrive(&bars.w_full[s]);
@@ -576,43 +613,60 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       __syncwarp();
       ++made;
     };
-    for (int k = 0;; ++k) {
+    while (true) {
+      for (int k = 0;; ++k) {
 #pragma unroll 1
-      while (more && made <= (k == 0 ? 0 : k + kAhead)) make();   // (the first piece's Q before its successors)
-      if (k >= made) break;
-      const Desc& d = bars.desc[k % kRing];               // (kept: this warp makes its successor in the ring)
-      if (!d.valid) break;
-      if (!ok) continue;
-      bool a = true;
-      if (nq > 0 && lane == 0) a = wait_for(&bars.q_empty, (nq - 1) & 1, abort);
-      ok = __all_sync(0xffffffffu, a);
-      if (!ok) continue;
-      if (lane == 0) {
-        // rows past the tensor's nodes read as zeros
-        mbar_expect_tx(&bars.q_full, static_cast<uint32_t>(npt * G) * D * 2);
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-          tma_load_4d(&map_q, base + Sh::kQ + h * kHalfBytes, &bars.q_full, 64 * h, d.g * G, d.i0, d.b);
-      }
-      ++nq;
-      if (d.ntr > 0) {
-        const int buf = ntree & 1;
-        if (ntree >= 2 && lane == 0) a = wait_for(&bars.t_empty[buf], ((ntree >> 1) - 1) & 1, abort);
+        while (more && made <= (k == 0 ? 0 : k + kAhead)) make(); // (the first piece's Q before its successors)
+        if (k >= made) break;
+        const Desc& d = bars.desc[k % kRing];             // (kept: this warp makes its successor in the ring)
+        if (!d.valid) break;
+        if (!ok) continue;
+        bool a = true;
+        if (nq > 0 && lane == 0) a = wait_for(&bars.q_empty, (nq - 1) & 1, going);
         ok = __all_sync(0xffffffffu, a);
         if (!ok) continue;
-        const int32_t* par = p.parent + d.b * p.par_sb;
-#pragma unroll 1
-        for (int j = lane; j < d.i0 + d.nodes; j += 32) {
-          const int pj = par[j];
-          spar[buf * kMaxT + j] = j == 0 ? (pj == -1 ? kRootMark : kBadMark)
-                                         : ((pj >= 0 && pj < j) ? static_cast<uint16_t>(pj) : kBadMark);
+        if (lane == 0) {
+          // rows past the tensor's nodes read as zeros
+          mbar_expect_tx(&bars.q_full, static_cast<uint32_t>(npt * G) * D * 2);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(&map_q, base + Sh::kQ + h * kHalfBytes, &bars.q_full, 64 * h, d.g * G, d.i0, d.b);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.t_full[buf]);
-        ++ntree;
+        ++nq;
+        if (d.ntr > 0) {
+          const int buf = ntree & 1;
+          if (ntree >= 2 && lane == 0) a = wait_for(&bars.t_empty[buf], ((ntree >> 1) - 1) & 1, going);
+          ok = __all_sync(0xffffffffu, a);
+          if (!ok) continue;
+          const int32_t* par = p.parent + d.b * p.par_sb;
+#pragma unroll 1
+          for (int j = lane; j < d.i0 + d.nodes; j += 32) {
+            const int pj = par[j];
+            spar[buf * kMaxT + j] = j == 0 ? (pj == -1 ? kRootMark : kBadMark)
+                                           : ((pj >= 0 && pj < j) ? static_cast<uint16_t>(pj) : kBadMark);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.t_full[buf]);
+          ++ntree;
+        }
       }
+      if (failed) break;
+      if (lane == 0 && nq > 0) drain(&bars.q_full, (nq - 1) & 1);
+      // the softmax warps have written their last row
+      bar_sync(4, kSoftmaxThreads + 32);
+      failed = __any_sync(0xffffffffu, *going == 0);
+      if (!failed) break;
+      // the other roles that wait for a description that will not come find an end
+      if (lane == 0) {
+        *static_cast<volatile int*>(&bars.desc[made % kRing].valid) = 0;
+        mbar_arrive(&bars.w_full[made % kRing]);
+      }
+      // the whole stretch again, every row NaN
+      pos = ln.first;
+      made = 0;
+      more = true;
+      if (lane == 0) set_status(p.status, TV_DEV_TIMEOUT);
     }
-    if (lane == 0 && nq > 0) drain(&bars.q_full, (nq - 1) & 1);
     if (lane == 0 && member == 0) p.splits[ln.stretch] = split;
     __syncwarp();
   } else if (warp == kWarpMma) {
@@ -627,13 +681,13 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       int cnt_s = 0, cnt_p = 0;                           // tiles of the present pieces
       int na = 0, keys0 = 0, nodes = 0, lo0 = 0, off = 0; // of the piece of the next P V
       auto next_s = [&]() {
-        ds = desc(++ks);
+        ds = desc(++ks, false);
         if (ds) cnt_s = ds->cnt;
         rs = 0;
       };
       auto next_p = [&]() {
         if (kp >= 0) release(kp);
-        dp = desc(++kp);
+        dp = desc(++kp, false);
         if (dp) {
           cnt_p = dp->cnt;
           na = dp->na; keys0 = dp->L - dp->a0 * kKeys; nodes = dp->n; lo0 = dp->lo0; off = dp->off;
@@ -642,6 +696,10 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       };
       next_s();
       next_p();
+      if (p.lost == kLostProducts && dp) {
+        dp = nullptr;
+        *going = 0;
+      }
       uint32_t idle = 0;
       while (dp) {
         const uint32_t par = static_cast<uint32_t>((is / KS) & 1) | static_cast<uint32_t>(ks & 1) << 1 |
@@ -698,19 +756,17 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         if (did) {
           idle = 0;
-        } else if (++idle >= kWaitLimit || ((idle & 255u) == 255u && *abort)) {
-          *abort = 1;
+        } else if (++idle >= kWaitLimit || ((idle & 255u) == 255u && *going == 0)) {
+          *going = 0;
           break;
         }
       }
-      if (*abort) {
+      if (*going == 0) {
         // what was issued completes before the TMEM is freed
 #pragma unroll 1
         for (int j = is > kSB ? is - kSB : 0; j < is; ++j) drain(&bars.s_full[j % kSB], (j / kSB) & 1);
 #pragma unroll 1
         for (int j = ip > 2 ? ip - 2 : 0; j < ip; ++j) drain(&bars.pv_done[j & 1], (j >> 1) & 1);
-#pragma unroll 1
-        while (dp) next_p();
       }
     }
     __syncwarp();
@@ -724,7 +780,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     int it0 = 0, ntree = 0, nfix = 0;                     // tiles, tree pieces, the group's tree tiles before this piece
     bool ok = true;
     for (int k = 0;; ++k) {
-      const Desc* d = desc(k);
+      const Desc* d = desc(k, true);
       if (!d) break;
       const int my_rows = d->nodes * G;
       const bool live = (warp & 3) * 32 < my_rows;        // the warp has valid rows
@@ -756,7 +812,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         if (tree) {
           if (cur == -2) {
-            ok = ok && __all_sync(0xffffffffu, wait_for(&bars.t_full[ntree & 1], (ntree >> 1) & 1, abort));
+            ok = ok && __all_sync(0xffffffffu, wait_for(&bars.t_full[ntree & 1], (ntree >> 1) & 1, going));
             cur = row_valid && ok ? my_node : -1;
           }
 #pragma unroll 1
@@ -769,7 +825,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             cur = up >= kRootMark ? -1 : static_cast<int>(up);
           }
         }
-        ok = ok && __all_sync(0xffffffffu, wait_for(&bars.s_full[sb], (it / kSB) & 1, abort));
+        ok = ok && __all_sync(0xffffffffu, wait_for(&bars.s_full[sb], (it / kSB) & 1, going));
         fence_after();
         if (live && ok) {
           // d = 64 masks S where it lies and reads it again for the weights, in
@@ -808,14 +864,14 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           // the row's reference maximum after the tile before
           float m = -INFINITY;
           if (r > 0) {
-            ok = __all_sync(0xffffffffu, wait_for(&bars.dec[warp & 3][half ^ 1], ((it - 1) >> 1) & 1, abort));
+            ok = __all_sync(0xffffffffu, wait_for(&bars.dec[warp & 3][half ^ 1], ((it - 1) >> 1) & 1, going));
             m = bars.m_ref[row];
           }
           const float m_new = fmaxf(m, mt);
           const bool grow = m_new > m + 8.0f;             // also the first finite maximum
           if (__any_sync(0xffffffffu, grow) && r > 0 && ok) {
             // O holds the tiles before this one: wait for the last P V, then rescale
-            ok = __all_sync(0xffffffffu, wait_for(&bars.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, abort));
+            ok = __all_sync(0xffffffffu, wait_for(&bars.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, going));
             fence_after();
             const float factor = grow ? ex2_approx(m - m_new) : 1.f;   // 0 when m = -inf
 #pragma unroll 1
@@ -873,7 +929,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         if (!full) {
           // V rows of the K steps that are no keys are cleared, nodes' rows looked over
-          ok = ok && __all_sync(0xffffffffu, wait_for(&bars.v_full[it % VS], (it / VS) & 1, abort));
+          ok = ok && __all_sync(0xffffffffu, wait_for(&bars.v_full[it % VS], (it / VS) & 1, going));
           uint8_t* v0 = gbase + Sh::kV + (it % VS) * TB;
           uint32_t* vbad = bars.vbad[half][nfix & 3];
           auto chunk = [&](int x, int ch) {
@@ -908,7 +964,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          // every warp of the group comes here for every tree tile, after an abort too
+          // every warp of the group comes here for every tree tile, whatever has happened
           if (tree) bar_sync(2 + half, 128);
         }
         if (tree) {
@@ -925,7 +981,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       }
       // ---------------------------------------------------------- output
       it0 += cnt;
-      ok = ok && __all_sync(0xffffffffu, wait_for(&bars.o_full, k & 1, abort));
+      ok = ok && __all_sync(0xffffffffu, wait_for(&bars.o_full, k & 1, going));
       // the groups' sums meet at the larger of their maxima, O's reference:
       // out = O / (2^(m_0 - M) l_0 + 2^(m_1 - M) l_1); group h writes half of the columns
       bars.red_m[half][row] = m_run;
@@ -978,7 +1034,7 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                   make_float4(v0[4 * e], v0[4 * e + 1], v0[4 * e + 2], v0[4 * e + 3]);
           }
         }
-        if (nf && row_valid) add_nonfinite<D>(p, *d, slot, orow, half * NC, NC, my_node, par, whole);
+        if (nf && row_valid && !bad) add_nonfinite<D>(p, *d, slot, orow, half * NC, NC, my_node, par, whole);
         if (half == 0 && row_valid) {
           const float lse2 = bad ? NAN : (empty ? -INFINITY : M + log2f(l_row));
           if (!whole) p.part_lse[slot] = lse2;
@@ -994,14 +1050,12 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (lane == 0) mbar_arrive(&bars.t_empty[ntree & 1]);
         ++ntree;
       }
-      if (tid == 0) {
-        if (bars.bad_piece[k & 7] == k + 1) set_status(p.status, TV_DEV_BAD_PAGE);
-        if (!ok) set_status(p.status, TV_DEV_TIMEOUT);
-      }
+      if (tid == 0 && bars.bad_piece[k & 7] == k + 1) set_status(p.status, TV_DEV_BAD_PAGE);
       bar_sync(1, kSoftmaxThreads);                       // red_*, m_ref: read by all
       __syncwarp();
       if (lane == 0) release(k);
     }
+    bar_arrive(4, kSoftmaxThreads + 32);                  // (warp 11)
   }
   fence_before();
   __syncthreads();
@@ -1029,7 +1083,11 @@ cudaError_t launch(const PagedAttnParams& p, int grid, const CUtensorMap* m, cud
   return cudaGetLastError();
 }
 
+std::atomic<int> g_lost{0};
+
 }  // namespace
+
+void attn_paged_set_lost(int lost) { g_lost = lost; }
 
 int attn_paged_tc_box(int P) {
   int b = 128;
@@ -1064,8 +1122,9 @@ bool attn_paged_tc_supported(const tv_attn_paged_args* a) {
   return (al & 15u) == 0 && tcmap::encode_fn() != nullptr;
 }
 
-cudaError_t launch_attn_paged_tc(const PagedAttnParams& p, int grid, cudaStream_t stream) {
+cudaError_t launch_attn_paged_tc(PagedAttnParams& p, int grid, cudaStream_t stream) {
   CUtensorMap m[5];
+  p.lost = g_lost;
   const int tile = kRows / p.G * p.G;
   auto map = [&](CUtensorMap* t, const void* x, int64_t d1, int64_t d2, int64_t d3, int64_t s1, int64_t s2, int64_t s3,
                  int b1, int b2) {

@@ -157,6 +157,12 @@ extern "C" tv_status tree_verify_attn_paged(const tv_attn_paged_args* a, void* w
   return from_cuda(launch_attn_paged_merge(p, pl.grid / pl.team, s));
 }
 
+extern "C" tv_status tv_attn_paged_set_lost(int32_t lost) {
+  if (lost < 0 || lost > 2) return TV_ERR_INVALID_ARG;
+  attn_paged_set_lost(lost);
+  return TV_OK;
+}
+
 // ------------------------------------------------------------ acceptance
 
 extern "C" tv_status tree_accept_probs(const tv_accept_probs_args* a, tv_stream_t stream) {

@@ -97,6 +97,8 @@ def bind(L):
         f.restype = c_size
     L.tree_accept_probs.argtypes = [ctypes.POINTER(AcceptProbsArgs), c_vp]
     L.tree_accept_probs.restype = ctypes.c_int
+    L.tv_attn_paged_set_lost.argtypes = [c_i32]
+    L.tv_attn_paged_set_lost.restype = ctypes.c_int
     L.tv_attn_paged_path.argtypes = [ctypes.POINTER(AttnPagedArgs)]
     L.tv_attn_paged_path.restype = c_i32
 
@@ -145,6 +147,12 @@ def tree_verify_attn_paged(q, k_pages, v_pages, page_table, prefix_len, k_tree, 
     None.  T = 1 decodes single tokens.  Returns (out, lse); rows past n_nodes[b] are not written."""
     return (_binding or binding()).attn(q, k_pages, v_pages, page_table, prefix_len, k_tree, v_tree, parent, n_nodes, scale,
                                         out, lse, want_lse, dev_status, _raw(stream, q), prefix_only)
+
+
+def attn_set_lost(lost: int) -> None:
+    """Test hook (tv_attn_paged_set_lost): calls behave as if a wait of the tensor-core kernel had run out, for the pieces
+    of work after a CTA's first (1) or for its products (2).  0 ends it."""
+    _tv._check(_tv.lib().tv_attn_paged_set_lost(int(lost)), "tv_attn_paged_set_lost")
 
 
 # --------------------------------------------------------------- acceptance
