@@ -1,0 +1,43 @@
+"""The paged cache's row moves at the largest pages and rows that are taken:
+two-byte words (an odd number of bf16 a row) whose counts come within a step
+of 2^31."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from tree_verification_verify_b200 import build
+    build.build()
+    yield
+    torch.cuda.empty_cache()                                # (tens of GB)
+
+
+def _random(*shape):
+    x = torch.empty(shape, dtype=torch.int16, device="cuda")
+    return x.random_(-32768, 32767).view(torch.bfloat16)
+
+
+def _same(a, b):
+    return torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compaction_of_the_largest_pages(in_place):
+    """Pages of 65534 * 33 * 993 = 2^31 - 2 elements: the one in use moves to the front, whole."""
+    import tree_verification_verify_b200 as tv
+    P, H, d = 65534, 33, 993
+    assert P * H * d == 2 ** 31 - 2
+    k, v = _random(2, P, H, d), _random(2, P, H, d)
+    table, st = _i32([[1]]), _i32([0])
+    out, used = tv.tree_pages_compact(k, v, table, _i32([P]), out=table if in_place else None, dev_status=st)
+    torch.cuda.synchronize()
+    assert out.tolist() == [[0]] and used.tolist() == [1] and st.item() == 0
+    assert _same(k[0], k[1]) and _same(v[0], v[1])

@@ -37,7 +37,7 @@ constexpr int kThreads = 256;
 constexpr int kPlanThreads = 1024;               // of one CTA of the plan
 constexpr int kPlanCtas = 8;                     // a portable cluster
 constexpr int kSmallThreads = 512;               // of a CTA that plans for itself
-constexpr int kSmallSlice = 4 * kSmallThreads;   // words of a page of a layer that a CTA copies at a time
+constexpr uint32_t kSmallSlice = 4 * kSmallThreads;   // words of a page of a layer that a CTA copies at a time
 constexpr int64_t kSmallEntries = 16384;
 constexpr int kSmallPages = 32768, kSmallSeqs = 256;
 constexpr int kTicketBytes = 64 * 1024;
@@ -61,24 +61,31 @@ __device__ __forceinline__ W ldw(const char* p) { return *reinterpret_cast<const
 template <typename W>
 __device__ __forceinline__ void stw(char* p, W v) { *reinterpret_cast<W*>(p) = v; }
 
-// Copies words [w0, w1) of `rows` rows from page address s to page address d
-// (byte offsets into k and v), by the calling CTA.
+// Words of a page of a layer; the host refuses pages of 2^31 elements.  Places
+// a slice or a step past the last word still fit 32 bits without a sign.
+template <typename W>
+__device__ __forceinline__ uint32_t page_words(const Pool& pl, int P) {
+  return static_cast<uint32_t>(P) * pl.Hkv * (pl.vec_bytes / static_cast<int>(sizeof(W)));
+}
+
+// Copies words [w0, w1) from page address s to page address d (byte offsets
+// into k and v), by the calling CTA.
 template <typename W, int NT>
-__device__ __forceinline__ void copy_words(const Pool& pl, int64_t d, int64_t s, int w0, int w1) {
-  const int wpv = pl.vec_bytes / static_cast<int>(sizeof(W));
-  const int wpr = wpv * pl.Hkv;
+__device__ __forceinline__ void copy_words(const Pool& pl, int64_t d, int64_t s, uint32_t w0, uint32_t w1) {
+  const uint32_t wpv = pl.vec_bytes / static_cast<uint32_t>(sizeof(W));
+  const uint32_t wpr = wpv * pl.Hkv;
   constexpr int U = 4;
-  for (int i0 = w0 + threadIdx.x; i0 < w1; i0 += U * NT) {
+  for (uint32_t i0 = w0 + threadIdx.x; i0 < w1; i0 += U * NT) {
     W a[U], b[U];
     int64_t off[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * NT;
+      const uint32_t i = i0 + u * NT;
       if (i < w1) {
         if (pl.dense) {
           off[u] = static_cast<int64_t>(i) * sizeof(W);
         } else {
-          const int r = i / wpr, h = i % wpr / wpv, w = i % wpv;
+          const uint32_t r = i / wpr, h = i % wpr / wpv, w = i % wpv;
           off[u] = r * pl.sr + h * pl.sh + static_cast<int64_t>(w) * sizeof(W);
         }
         a[u] = ldw<W>(pl.k + s + off[u]);
@@ -592,12 +599,13 @@ __global__ void __launch_bounds__(kSmallThreads) update_small_kernel(UpdateParam
     }
   }
   if (fail) return;
-  const int wpr = p.pool.Hkv * (p.pool.vec_bytes / static_cast<int>(sizeof(W)));         // words of a row
+  const uint32_t wpr = page_words<W>(p.pool, 1);   // words of a row
   const int slices = small_slices(p.P, wpr);
   const int64_t jobs = static_cast<int64_t>(n_copies) * p.layers * slices;
   for (int64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
-    const int b = s_list[j / (p.layers * slices)], rest = static_cast<int>(j % (p.layers * slices));
-    const int layer = rest / slices, w0 = rest % slices * kSmallSlice;
+    const int64_t k = j / slices;                // the copy's layer
+    const int b = s_list[k / p.layers], layer = static_cast<int>(k % p.layers);
+    const uint32_t w0 = static_cast<uint32_t>(j % slices) * kSmallSlice;
     copy_words<W, NT>(p.pool, layer * p.pool.sl + select_bit(before, words, s_off[b], free_word) * p.pool.sp,
                       layer * p.pool.sl + s_page[b] * p.pool.sp, w0,
                       min(s_turn[b].keep % p.P * wpr, w0 + kSmallSlice));
@@ -725,7 +733,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CompactParam
 
 // The tables' new names, then the pages, split over the grid in slices of
 // kSliceWords words of a page of one layer.
-constexpr int kSliceWords = 4 * kThreads;
+constexpr uint32_t kSliceWords = 4 * kThreads;
 
 template <typename W>
 __global__ void __launch_bounds__(kThreads) compact_apply_kernel(CompactParams p) {
@@ -741,13 +749,13 @@ __global__ void __launch_bounds__(kThreads) compact_apply_kernel(CompactParams p
       p.out[b * p.po_sb + i] = page;
     }
   }
-  const int words = p.P * p.pool.Hkv * (p.pool.vec_bytes / static_cast<int>(sizeof(W)));
-  const int slices = (words + kSliceWords - 1) / kSliceWords;
+  const uint32_t words = page_words<W>(p.pool, p.P);
+  const int slices = static_cast<int>((words + kSliceWords - 1) / kSliceWords);
   const int64_t jobs = static_cast<int64_t>(moves) * p.layers * slices;
   for (int64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
-    const int m = static_cast<int>(j / (p.layers * slices));
-    const int rest = static_cast<int>(j % (p.layers * slices));
-    const int layer = rest / slices, w0 = rest % slices * kSliceWords;
+    const int64_t k = j / slices;                // the move's layer
+    const int m = static_cast<int>(k / p.layers), layer = static_cast<int>(k % p.layers);
+    const uint32_t w0 = static_cast<uint32_t>(j % slices) * kSliceWords;
     copy_words<W, kThreads>(p.pool, layer * p.pool.sl + p.to[m] * p.pool.sp, layer * p.pool.sl + p.from[m] * p.pool.sp, w0,
                   min(words, w0 + kSliceWords));
   }
@@ -819,13 +827,13 @@ __global__ void __launch_bounds__(kSmallThreads) compact_small_kernel(CompactPar
     }
     p.out[b * p.po_sb + i] = page;
   }
-  const int wpp = p.P * p.pool.Hkv * (p.pool.vec_bytes / static_cast<int>(sizeof(W)));   // words of a page of a layer
-  const int slices = (wpp + kSmallSlice - 1) / kSmallSlice;
+  const uint32_t wpp = page_words<W>(p.pool, p.P);
+  const int slices = static_cast<int>((wpp + kSmallSlice - 1) / kSmallSlice);
   const int64_t jobs = static_cast<int64_t>(n) * p.layers * slices;
   for (int64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
-    const int m = static_cast<int>(j / (p.layers * slices));
-    const int rest = static_cast<int>(j % (p.layers * slices));
-    const int layer = rest / slices, w0 = rest % slices * kSmallSlice;
+    const int64_t k = j / slices;                // the move's layer
+    const int m = static_cast<int>(k / p.layers), layer = static_cast<int>(k % p.layers);
+    const uint32_t w0 = static_cast<uint32_t>(j % slices) * kSmallSlice;
     const int from = select_bit(moves, words, m, move_word), to = select_bit(holes, words, m, hole_word);
     copy_words<W, NT>(p.pool, layer * p.pool.sl + to * p.pool.sp, layer * p.pool.sl + from * p.pool.sp, w0,
                       min(wpp, w0 + kSmallSlice));
