@@ -41,3 +41,19 @@ def test_compaction_of_the_largest_pages(in_place):
     torch.cuda.synchronize()
     assert out.tolist() == [[0]] and used.tolist() == [1] and st.item() == 0
     assert _same(k[0], k[1]) and _same(v[0], v[1])
+
+
+def test_commit_of_the_widest_rows():
+    """256 rows of 2^23 two-byte words: 2^31 of them in one path."""
+    import tree_verification_verify_b200 as tv
+    T, H = 256, 2 ** 23
+    kt, vt = _random(1, T, H, 1), _random(1, T, H, 1)
+    k, v = (torch.zeros(T, 1, H, 1, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    order = torch.randperm(T, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    acc = torch.cat([torch.arange(1, T, dtype=torch.int32, device="cuda"), _i32([-1])])[None]
+    n = tv.tree_commit_kv_paged(k, v, order[None], _i32([0]), kt, vt, _i32([T - 1]), acc)
+    torch.cuda.synchronize()
+    assert n.tolist() == [T]
+    for pool, tree in ((k, kt), (v, vt)):
+        for r in range(T):
+            assert _same(pool[order[r]], tree[0, r][None])

@@ -217,9 +217,10 @@ struct CommitPagedParams {
   const int32_t* acc; int64_t acc_sb;
   int32_t* tickets;
   uint32_t* status;
+  int step;                                      // path rows at a time: their words are fewer than 2^31
 };
 
-constexpr int kCommitRows = 256;                 // path rows looked up at a time
+constexpr int kCommitRows = 256;                 // path rows looked up at a time, at most
 
 // One CTA per (sequence, layer).  Path row r goes from tree node rows[r] to
 // row (L + r) % P of page table[(L + r) / P]; the rows' addresses are looked
@@ -252,10 +253,10 @@ __global__ void __launch_bounds__(kThreads) commit_paged_kernel(CommitPagedParam
   if (tid == 0 && layer == 0 && !ok)
     set_status(p.status, !ok_len ? TV_DEV_BAD_LEN : (bad_row ? TV_DEV_BAD_ROW : 0u) | (bad_page ? TV_DEV_BAD_PAGE : 0u));
   if (ok) {
-    const int wpv = p.pool.vec_bytes / static_cast<int>(sizeof(W));
-    const int wpr = wpv * p.pool.Hkv;
-    for (int r0 = 0; r0 <= n; r0 += kCommitRows) {
-      const int rows = min(kCommitRows, n + 1 - r0);
+    const uint32_t wpv = p.pool.vec_bytes / static_cast<uint32_t>(sizeof(W));
+    const uint32_t wpr = wpv * p.pool.Hkv;
+    for (int r0 = 0; r0 <= n; r0 += p.step) {
+      const int rows = min(p.step, n + 1 - r0);
       if (r0 > 0) {
         __syncthreads();
         if (tid < rows) {
@@ -265,8 +266,8 @@ __global__ void __launch_bounds__(kThreads) commit_paged_kernel(CommitPagedParam
         }
         __syncthreads();
       }
-      for (int i = tid; i < rows * wpr; i += kThreads) {
-        const int r = i / wpr, h = i % wpr / wpv, w = i % wpv;
+      for (uint32_t i = tid; i < rows * wpr; i += kThreads) {
+        const uint32_t r = i / wpr, h = i % wpr / wpv, w = i % wpv;
         const int64_t s = layer * p.tl + s_src[r] + h * p.th + static_cast<int64_t>(w) * sizeof(W);
         const int64_t d = layer * p.pool.sl + s_dst[r] + h * p.pool.sh + static_cast<int64_t>(w) * sizeof(W);
         const W kw = ldw<W>(p.kt + s), vw = ldw<W>(p.vt + s);
@@ -964,7 +965,9 @@ cudaError_t launch_commit_paged(const tv_commit_paged_args* a, void* ws, cudaStr
   p.status = a->dev_status;
   const Pool& o = p.pool;
   const dim3 grid(static_cast<unsigned>(a->B), static_cast<unsigned>(a->layers));
-  switch (word_bytes({o.k, o.v, p.kt, p.vt}, {o.sl, o.sp, o.sr, o.sh, o.vec_bytes, p.tl, p.tb, p.tt, p.th})) {
+  const int w = word_bytes({o.k, o.v, p.kt, p.vt}, {o.sl, o.sp, o.sr, o.sh, o.vec_bytes, p.tl, p.tb, p.tt, p.th});
+  p.step = static_cast<int>(std::min<int64_t>(kCommitRows, INT32_MAX / (static_cast<int64_t>(a->Hkv) * (o.vec_bytes / w))));
+  switch (w) {
     case 16: commit_paged_kernel<uint4><<<grid, kThreads, 0, stream>>>(p); break;
     case 4: commit_paged_kernel<uint32_t><<<grid, kThreads, 0, stream>>>(p); break;
     default: commit_paged_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(p); break;
