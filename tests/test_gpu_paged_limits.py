@@ -57,3 +57,26 @@ def test_commit_of_the_widest_rows():
     for pool, tree in ((k, kt), (v, vt)):
         for r in range(T):
             assert _same(pool[order[r]], tree[0, r][None])
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Sizes that would wrap in the C ABI's 32-bit fields, as views of little memory where that is possible."""
+    import tree_verification_verify_b200 as tv
+    big = 2 ** 32
+    page = torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    pool = page.expand(big + 3, 4, 1, 64)
+    layers = page[None].expand(big + 1, 1, 4, 1, 64)
+    tree, q = page[:, :1], torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    table, one = _i32([[0]]), _i32([1])
+    with pytest.raises(tv.TVError, match="num_pages"):
+        tv.tree_verify_attn_paged(q, pool, pool, table, one, tree, tree, _i32([[-1]]))
+    with pytest.raises(tv.TVError, match="num_pages"):
+        tv.tree_commit_kv_paged(pool, pool, table, one, tree, tree, _i32([0]), _i32([[-1]]))
+    with pytest.raises(tv.TVError, match="layers"):
+        tv.tree_pages_update(layers, layers, table, _i32([0]), one, one)
+    with pytest.raises(tv.TVError, match="layers"):
+        tv.tree_pages_compact(layers, layers, table, one)
+    p = torch.zeros(1, 1, big + 5, device="cuda")
+    u = torch.zeros(1, 1, dtype=torch.float64, device="cuda")
+    with pytest.raises(tv.TVError, match="V must be"):
+        tv.tree_accept_probs(p, _i32([[0]]), _i32([[-1]]), u, u)

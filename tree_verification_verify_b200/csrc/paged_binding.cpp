@@ -87,6 +87,12 @@ const at::Tensor* opt(PyObject* o, const char* name, Device& dev) {
   return t;
 }
 
+// A size for one of the ABI's 32-bit fields.
+int32_t i32(int64_t size, const char* name) {
+  if (size > INT32_MAX) refuse("%s must be below 2^31", name);
+  return static_cast<int32_t>(size);
+}
+
 bool is_shape(const at::Tensor& t, at::IntArrayRef s) { return t.sizes() == s; }
 
 int dtype(const at::Tensor& t, const char* name) {
@@ -251,12 +257,12 @@ PyObject* attn(PyObject*, PyObject* const* v, Py_ssize_t n) {
     }
     need(!lse || (is_shape(*lse, {B, T, Hq}) && lse->scalar_type() == at::kFloat && lse->is_contiguous()),
          "lse must be contiguous fp32 [B][T][Hq]");
-    a.B = B; a.T = T; a.Hq = Hq; a.Hkv = k.size(2); a.d = d;
-    a.num_pages = k.size(0); a.page_size = k.size(1);
+    a.B = i32(B, "B"); a.T = i32(T, "T"); a.Hq = i32(Hq, "Hq"); a.Hkv = i32(k.size(2), "Hkv"); a.d = i32(d, "d");
+    a.num_pages = i32(k.size(0), "num_pages"); a.page_size = i32(k.size(1), "page_size");
     a.q = q.data_ptr(); a.q_sb = q.stride(0); a.q_st = q.stride(1); a.q_sh = q.stride(2);
     a.k_pages = k.data_ptr(); a.v_pages = vp.data_ptr();
     a.kv_sp = k.stride(0); a.kv_sr = k.stride(1); a.kv_sh = k.stride(2);
-    a.page_table = table(pt, B, -1, "page_table"); a.pt_sb = pt.stride(0); a.max_pages = pt.size(1);
+    a.page_table = table(pt, B, -1, "page_table"); a.pt_sb = pt.stride(0); a.max_pages = i32(pt.size(1), "max_pages");
     a.prefix_len = vec(&len, B, "prefix_len");
     a.k_tree = kt.data_ptr(); a.v_tree = vt.data_ptr();
     a.kt_sb = kt.stride(0); a.kt_st = kt.stride(1); a.kt_sh = kt.stride(2);
@@ -310,7 +316,7 @@ PyObject* accept(PyObject*, PyObject* const* v, Py_ssize_t n) {
       need(!u || (u->scalar_type() == at::kDouble && is_shape(*u, {B, T}) && u->is_contiguous()),
            "u_child and u_sample must be contiguous fp64 [B][T]");
     tv_accept_probs_args a = {};
-    a.B = B; a.T = T; a.V = V;
+    a.B = i32(B, "B"); a.T = i32(T, "T"); a.V = i32(V, "V");
     a.target_probs = static_cast<const float*>(p.data_ptr()); a.tp_sb = p.stride(0); a.tp_st = p.stride(1);
     if (q) {
       a.draft_probs = static_cast<const float*>(q->data_ptr()); a.dp_sb = q->stride(0); a.dp_st = q->stride(1);
@@ -362,8 +368,9 @@ Layers pool(A& a, const at::Tensor& k, const at::Tensor& v) {
   need(k.dim() == 4 || k.dim() == 5, "the pool must be [num_pages][page_size][Hkv][d], with a leading layer dimension or not");
   pair(k, v, "the pool's");
   const Layers l(k);
-  a.layers = l.n; a.kv_sl = l.stride;
-  a.num_pages = k.size(l.at); a.page_size = k.size(l.at + 1); a.Hkv = k.size(l.at + 2); a.d = k.size(l.at + 3);
+  a.layers = i32(l.n, "layers"); a.kv_sl = l.stride;
+  a.num_pages = i32(k.size(l.at), "num_pages"); a.page_size = i32(k.size(l.at + 1), "page_size");
+  a.Hkv = i32(k.size(l.at + 2), "Hkv"); a.d = i32(k.size(l.at + 3), "d");
   a.kv_sp = k.stride(l.at); a.kv_sr = k.stride(l.at + 1); a.kv_sh = k.stride(l.at + 2);
   a.k_pages = k.data_ptr(); a.v_pages = v.data_ptr();
   return l;
@@ -394,10 +401,10 @@ PyObject* commit(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const int64_t B = kt.size(t.at), T = kt.size(t.at + 1);
     need(kt.scalar_type() == k.scalar_type() && t.n == l.n && kt.size(t.at + 2) == a.Hkv && kt.size(t.at + 3) == a.d,
          "tree K/V must be [layers][B][T][Hkv][d] of the pool's dtype");
-    a.B = B; a.T = T;
+    a.B = i32(B, "B"); a.T = i32(T, "T");
     a.k_tree = kt.data_ptr(); a.v_tree = vt.data_ptr();
     a.kt_sl = t.stride; a.kt_sb = kt.stride(t.at); a.kt_st = kt.stride(t.at + 1); a.kt_sh = kt.stride(t.at + 2);
-    a.page_table = table(pt, B, -1, "page_table"); a.pt_sb = pt.stride(0); a.max_pages = pt.size(1);
+    a.page_table = table(pt, B, -1, "page_table"); a.pt_sb = pt.stride(0); a.max_pages = i32(pt.size(1), "max_pages");
     a.prefix_len = vec(&len, B, "prefix_len");
     a.prefix_len_out = lo ? vec(lo, B, "prefix_len_out") : vec(&len, B, "prefix_len");
     a.n_accepted = vec(&na, B, "n_accepted");
@@ -441,7 +448,7 @@ PyObject* update(PyObject*, PyObject* const* v, Py_ssize_t n) {
     pool(a, k, vp);
     need(pt.dim() == 2 && src.dim() == 1, "page_table must be [B_in][max_pages], source [B]");
     const int64_t B = src.size(0);
-    a.B_in = pt.size(0); a.max_pages_in = pt.size(1); a.B = B;
+    a.B_in = i32(pt.size(0), "B_in"); a.max_pages_in = i32(pt.size(1), "max_pages"); a.B = i32(B, "B");
     a.page_table = table(pt, pt.size(0), -1, "page_table"); a.pt_sb = pt.stride(0);
     a.source = vec(&src, B, "source"); a.keep = vec(&keep, B, "keep"); a.grow = vec(&grow, B, "grow");
     a.pinned = vec(pin, a.num_pages, "pinned");
@@ -454,7 +461,7 @@ PyObject* update(PyObject*, PyObject* const* v, Py_ssize_t n) {
       nf_new = at.empty({1}, at::kInt);
       nf = &nf_new;
     }
-    a.page_table_out = table(*out, B, -1, "out"); a.po_sb = out->stride(0); a.max_pages = out->size(1);
+    a.page_table_out = table(*out, B, -1, "out"); a.po_sb = out->stride(0); a.max_pages = i32(out->size(1), "max_pages");
     a.n_free = vec(nf, 1, "n_free");
     a.dev_status = status_word(st);
     run(at, "tree_pages_update", a, g_fn.update, g_fn.update_ws);
@@ -480,7 +487,7 @@ PyObject* compact(PyObject*, PyObject* const* v, Py_ssize_t n) {
     pool(a, k, vp);
     need(pt.dim() == 2, "page_table must be [B][max_pages]");
     const int64_t B = pt.size(0);
-    a.B = B; a.max_pages = pt.size(1);
+    a.B = i32(B, "B"); a.max_pages = i32(pt.size(1), "max_pages");
     a.page_table = table(pt, B, -1, "page_table"); a.pt_sb = pt.stride(0);
     a.length = vec(&len, B, "length");
     a.pinned = vec(pin, a.num_pages, "pinned");
