@@ -158,6 +158,7 @@ def attn_set_lost(lost: int) -> None:
 # --------------------------------------------------------------- acceptance
 
 _PROB_MODES = {"auto": 0, "specsample": 2, "specexec": 3}
+_PROB_OUTPUTS = ("n_accepted", "accepted_nodes", "out_tokens")
 
 
 def tree_accept_probs(target_probs, draft_tokens, parent, u_child, u_sample, draft_probs=None, n_nodes=None,
@@ -165,14 +166,18 @@ def tree_accept_probs(target_probs, draft_tokens, parent, u_child, u_sample, dra
     """Acceptance walk from given probabilities and random numbers (include/tree_verify.h, tree_accept_probs).
     target_probs, draft_probs fp32 [B][T][V] with contiguous rows; draft_tokens, parent int32 [B][T]; u_child (the test
     of each node; None for "specexec") and u_sample (the sample at each node) fp64 [B][T] in [0, 1).  Returns a dict of
-    device tensors n_accepted [B], accepted_nodes [B][T], out_tokens [B][T+1]."""
+    device tensors n_accepted [B], accepted_nodes [B][T], out_tokens [B][T+1]: `outputs` where it holds all three, else
+    a new dict with those that it lacks made."""
     if mode not in _PROB_MODES:
         raise _tv.TVError(f"mode must be one of {sorted(_PROB_MODES)}")
     o = outputs or {}
     r = (_binding or binding()).accept(target_probs, draft_tokens, parent, u_child, u_sample, draft_probs, n_nodes,
-                                       _PROB_MODES[mode], dev_status, _raw(stream, target_probs), o.get("n_accepted"),
-                                       o.get("accepted_nodes"), o.get("out_tokens"))
-    return outputs or dict(zip(("n_accepted", "accepted_nodes", "out_tokens"), r))
+                                       _PROB_MODES[mode], dev_status, _raw(stream, target_probs),
+                                       *[o.get(n) for n in _PROB_OUTPUTS])
+    made = dict(zip(_PROB_OUTPUTS, r))
+    if not outputs:
+        return made
+    return outputs if all(o.get(n) is not None for n in _PROB_OUTPUTS) else {**outputs, **made}
 
 
 # --------------------------------------------------------------- KV commit
