@@ -40,3 +40,17 @@ def test_acceptance_returns_every_output_whichever_are_given():
                 assert k not in given or got[k] is given[k]
     whole = {k: torch.empty_like(v) for k, v in want.items()}
     assert tv.tree_accept_probs(*args, **kw, outputs=whole) is whole
+
+
+def test_device_memory_that_runs_out_is_torchs_error():
+    """An output of 2^40 bytes cannot be made (its inputs are views of little memory); the next call is as ever."""
+    import tree_verification_verify_b200 as tv
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    B, T = 2 ** 20, 64
+    x = torch.zeros(1, 1, 1, 128, dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros(1, 16, 1, 128, dtype=torch.bfloat16, device="cuda")
+    q, tree = x.expand(B, T, 64, 128), x.expand(B, T, 1, 128)
+    with pytest.raises(torch.OutOfMemoryError):
+        tv.tree_verify_attn_paged(q, pool, pool, i32(B, 1), i32(B), tree, tree, i32(1, T).expand(B, T))
+    out, _ = tv.tree_verify_attn_paged(x, pool, pool, i32(1, 1), i32(1) + 3, x, x, i32(1, 1) - 1)
+    assert (out == 0).all()

@@ -3,6 +3,7 @@
 // where the launch itself takes 4 (a decoding step makes a few such calls per
 // layer).  The library's functions are handed in as addresses by
 // init(functions, error); nothing of the library is linked here.
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
@@ -192,12 +193,15 @@ PyObject* same(PyObject* o) {
   return o;
 }
 
-// Converts what a call throws; no exception leaves this file.
+// Converts what a call throws; no exception leaves this file.  Running out of
+// memory is torch's own error, as from any of its allocations.
 template <typename F>
 PyObject* guarded(F&& f) {
   try {
     return f();
   } catch (const Refused&) {
+  } catch (const c10::OutOfMemoryError&) {
+    torch::translate_exception_to_python(std::current_exception());
   } catch (const std::exception& e) {
     if (!PyErr_Occurred()) PyErr_SetString(g_error ? g_error : PyExc_RuntimeError, e.what());
   }
