@@ -27,6 +27,7 @@ NVCC_FLAGS = [
 
 BINDING = os.path.join(HERE, "_paged.so")
 BINDING_SRC = os.path.join(CSRC, "paged_binding.cpp")
+BINDING_FOR = os.path.join(HERE, "_build", "paged_binding.txt")     # what the binding was built against
 
 
 def sources():
@@ -46,6 +47,23 @@ def _headers():
 
 def _stale() -> bool:
     return _older(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + _headers())
+
+
+def binding_against() -> str:
+    """The torch and Python whose binary interfaces the binding uses."""
+    import torch
+    return f"torch {torch.__version__} python {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_built_against() -> str:
+    if not os.path.exists(BINDING_FOR):
+        return ""
+    with open(BINDING_FOR) as f:
+        return f.read()
+
+
+def _binding_stale() -> bool:
+    return _older(BINDING, [BINDING_SRC] + _headers()) or binding_built_against() != binding_against()
 
 
 def binding_command(out: str):
@@ -68,7 +86,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     jobs = []
     if force or _stale():
         jobs.append((LIB, [nvcc] + NVCC_FLAGS + ["-I", os.path.join(ROOT, "include")] + sources() + ["-o", LIB + ".tmp"]))
-    if force or _older(BINDING, [BINDING_SRC] + _headers()):
+    if force or _binding_stale():
         jobs.append((BINDING, binding_command(BINDING + ".tmp")))
     procs = []
     for _, cmd in jobs:
@@ -79,6 +97,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if p.wait() != 0:
             raise subprocess.CalledProcessError(p.returncode, cmd)
         os.replace(out + ".tmp", out)
+        if out == BINDING:
+            os.makedirs(os.path.dirname(BINDING_FOR), exist_ok=True)
+            with open(BINDING_FOR, "w") as f:
+                f.write(binding_against())
     return LIB
 
 
