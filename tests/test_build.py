@@ -1,6 +1,7 @@
 """The build: what is rebuilt when, and what a failure leaves."""
 
 import os
+import subprocess
 
 import pytest
 
@@ -62,3 +63,26 @@ def test_a_binding_of_another_torch_is_not_loaded(monkeypatch):
     monkeypatch.setattr(torch, "__version__", "99.1")
     with pytest.raises(tv.TVError, match="99.1.*build it again"):
         tv.paged.binding()
+
+
+def test_the_library_stands_by_itself(tools, monkeypatch):
+    """Without a C++ compiler, or with one that fails, the library is built and the user warned."""
+    for cxx in (tools("cxx_fails", before="exit 1\n"), "/nonexistent/cxx"):
+        monkeypatch.setenv("CXX", cxx)
+        with pytest.warns(UserWarning, match="binding of the paged calls was not built"):
+            assert b.build(force=True) == b.LIB
+        assert os.path.exists(b.LIB) and not os.path.exists(b.BINDING)
+        os.remove(b.LIB)
+    monkeypatch.setenv("CXX", tools("cxx"))
+    tools.runs()
+    b.build()
+    assert tools.runs() == ["cxx", "nvcc"] and os.path.exists(b.BINDING)
+
+
+def test_a_failed_library_leaves_nothing_running(tools, monkeypatch, tmp_path):
+    """The error comes when the other compiler has ended, and its output is in place."""
+    monkeypatch.setenv("NVCC", tools("nvcc_fails", before="exit 1\n"))
+    monkeypatch.setenv("CXX", tools("cxx_slow", before="sleep 1\n", after=f"echo end > {tmp_path}/ended"))
+    with pytest.raises(subprocess.CalledProcessError):
+        b.build()
+    assert (tmp_path / "ended").exists() and os.path.exists(b.BINDING) and not os.path.exists(b.LIB)

@@ -12,6 +12,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -79,28 +80,46 @@ def binding_command(out: str):
          "-lc10_cuda", "-L" + os.path.join(cuda, "lib64"), "-lcudart"]
 
 
+def _run(jobs, verbose: bool):
+    """The commands of (output, command), at the same time; each output that was made is put in place.  Returns the
+    errors by output, when all have ended."""
+    procs, errors = [], {}
+    for out, cmd in jobs:
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        try:
+            procs.append((out, cmd, subprocess.Popen(cmd)))
+        except OSError as e:
+            errors[out] = e
+    for out, cmd, p in procs:
+        if p.wait() != 0:
+            errors[out] = subprocess.CalledProcessError(p.returncode, cmd)
+        else:
+            os.replace(out + ".tmp", out)
+    return errors
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the CUDA sources into one shared library, and the binding
-    (each skipped when up to date).  Returns the library path."""
+    (each skipped when up to date).  Returns the library path.  The library
+    stands by itself: without a C++ compiler or Python's headers the binding
+    is left out with a warning, and the paged calls of the package say so."""
     nvcc = os.environ.get("NVCC", "nvcc")
     jobs = []
     if force or _stale():
         jobs.append((LIB, [nvcc] + NVCC_FLAGS + ["-I", os.path.join(ROOT, "include")] + sources() + ["-o", LIB + ".tmp"]))
-    if force or _binding_stale():
+    binding = force or _binding_stale()
+    if binding:
         jobs.append((BINDING, binding_command(BINDING + ".tmp")))
-    procs = []
-    for _, cmd in jobs:
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        procs.append(subprocess.Popen(cmd))
-    for (out, cmd), p in zip(jobs, procs):
-        if p.wait() != 0:
-            raise subprocess.CalledProcessError(p.returncode, cmd)
-        os.replace(out + ".tmp", out)
-        if out == BINDING:
-            os.makedirs(os.path.dirname(BINDING_FOR), exist_ok=True)
-            with open(BINDING_FOR, "w") as f:
-                f.write(binding_against())
+    errors = _run(jobs, verbose)
+    if LIB in errors:
+        raise errors[LIB]
+    if BINDING in errors:
+        warnings.warn(f"the binding of the paged calls was not built ({errors[BINDING]}); {LIB} was")
+    elif binding:
+        os.makedirs(os.path.dirname(BINDING_FOR), exist_ok=True)
+        with open(BINDING_FOR, "w") as f:
+            f.write(binding_against())
     return LIB
 
 
