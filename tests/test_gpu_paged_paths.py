@@ -111,3 +111,32 @@ def _not_finite(c, ref, hit, what):
     assert np.all(np.abs(o - ref["out"])[fine] <= ref["bound"][fine])
     assert hit.any() and not np.isfinite(o[hit]).any()
     assert (o[~ref["written"]] == 7).all()
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("L", [40, 9001])
+def test_a_value_that_is_not_finite_shows_however_small_its_weight(L, dtype, what):
+    """Weights of e^-400 are 0 in fp32; the value is a key's that the row sees, in one piece of work or in many."""
+    d, col = 64, 9
+    c = AttnCase(1, 3, 4, 1, d, 16, [L], dtype, tree="chain", poison=False)
+    c.q.fill_(1)                                            # scores are sums of K over 8
+    c.k.fill_(25)                                           # prefix 200
+    c.kt.fill_(-25)                                         # tree -200
+    c.vt[0, 1, 0, col] = what
+    out, lse, st = _run(c)
+    assert st == 0
+    o = out.double().cpu().numpy()
+    hit = np.zeros(o.shape, bool)
+    hit[0, 1:, :, col] = True
+    assert np.isfinite(o[~hit]).all() and not np.isfinite(o[hit]).any()
+    # a prefix key
+    c.vt[0, 1, 0, col] = 0
+    c.k.fill_(-25)
+    c.kt.fill_(25)
+    j = L // 2
+    c.v[c.table[0, j // 16], j % 16, 0, col] = what
+    out, lse, st = _run(c)
+    o = out.double().cpu().numpy()
+    hit[0, :, :, col] = True
+    assert np.isfinite(o[~hit]).all() and not np.isfinite(o[hit]).any()

@@ -215,7 +215,9 @@ attn_paged_simt_kernel(PagedAttnParams p, int vec) {
           float sum = 0.f;
 #pragma unroll
           for (int i = 0; i < KPL; ++i) {
-            const float e = expf(s[r][i] - base);
+            float e = expf(s[r][i] - base);
+            // (a key that the row sees has some weight: fp32's least, so that V shows if it is not finite)
+            if (tree && e == 0.f && s[r][i] > -INFINITY) e = 0x1p-149f;
             if (lane % LPK == 0) {
               ps[(warp * 4 + r) * KW + lane / LPK + i * 32] = e;
               sum += e;
@@ -358,10 +360,9 @@ __global__ void __launch_bounds__(kThreads) attn_paged_merge_kernel(PagedAttnPar
       if (k0 + i > u.c1) break;
       const float w = exp2f(v[i] - m);
       den += w;
-      if (w != 0.f) {
+      // (a piece without keys has 0 there; one whose weight is below fp32's range still shows what is not finite)
 #pragma unroll
-        for (int e = 0; e < DL; ++e) acc[e] = fmaf(w, o[i][e], acc[e]);
-      }
+      for (int e = 0; e < DL; ++e) acc[e] = fmaf(w, o[i][e], acc[e]);
     }
     M = m;
   }
