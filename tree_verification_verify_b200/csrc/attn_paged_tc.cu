@@ -828,12 +828,11 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         ok = ok && __all_sync(0xffffffffu, wait_for(&bars.s_full[sb], (it / kSB) & 1, going));
         fence_after();
         if (live && ok) {
-          // d = 64 masks S where it lies and reads it again for the weights, in
-          // loops, a quarter of the code: 256 sequences' single tokens on 400
-          // to 700 rows 208 us, so 170, the other shapes within 2 %.  With d =
-          // 128 the longer waits for TMEM cost what the code saves.
-          constexpr bool kAgain = D == 64;
-          if (kAgain && !full) {
+          // S is masked where it lies and read again for the weights, in loops, a
+          // quarter of the code of holding it in registers: 256 sequences' single
+          // tokens 162 us for 179 with d = 128, 171 for 210 with d = 64; 64
+          // sequences' single tokens 193 for 198, trees the same.
+          if (!full) {
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
               const uint32_t w = q < 2 ? (q == 0 ? mk[0] : mk[1]) : (q == 2 ? mk[2] : mk[3]);
@@ -851,10 +850,6 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32(scol + q * 32, s + q * 32);
           tmem_wait_ld();
-          if (!kAgain && !full) {
-#pragma unroll
-            for (int x = 0; x < 128; ++x) s[x] = ((mk[x >> 5] >> (x & 31)) & 1u) ? s[x] : -INFINITY;
-          }
           float mx[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) mx[x] = fmaxf(s[x], s[x + 8]);
@@ -897,8 +892,12 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           // p = 2^(s sl2 - m) as bf16 pairs over the first half of S
           float2 ps[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
           const float2 sl = make_float2(sl2, sl2), nm = make_float2(nmu, nmu);
-          auto weigh = [&](int q, const float* z) {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float z[32];
             uint32_t pk[16];
+            tmem_ld32(scol + q * 32, z);
+            tmem_wait_ld();
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
               float2 e = fma2(make_float2(z[x], z[x + 1]), sl, nm);
@@ -908,18 +907,6 @@ attn_paged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
               pk[x / 2] = pack_bf16(e.x, e.y);
             }
             tmem_st16u(scol + q * 16, pk);
-          };
-          if constexpr (kAgain) {
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              float z[32];
-              tmem_ld32(scol + q * 32, z);
-              tmem_wait_ld();
-              weigh(q, z);
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) weigh(q, s + q * 32);
           }
           const float2 sum = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
           l_run += sum.x + sum.y;
