@@ -24,7 +24,9 @@ def _lens(B, lo, hi):
 
 # B, T, Hq, Hkv, d, P, lens, n_nodes
 TEAMS = [
-    (48, 40, 64, 8, 128, 16, _lens(48, 20, 90), None),                          # three row tiles on a team of four
+    (48, 40, 64, 8, 128, 16, _lens(48, 20, 90), None),                          # three row tiles
+    (30, 70, 64, 8, 128, 16, _lens(30, 20, 90), None),                          # five: four of a team, then one
+    (48, 40, 64, 8, 128, 16, _lens(48, 20, 90), [(40, 16, 30)[b % 3] for b in range(48)]),
     (96, 20, 64, 8, 128, 16, _lens(96, 100, 200), [(20, 12)[b % 2] for b in range(96)]),
     (96, 20, 64, 8, 128, 5, _lens(96, 100, 200), [(20, 12)[b % 2] for b in range(96)]),   # rows copied one by one
     (96, 20, 64, 8, 64, 1, _lens(96, 1, 40), [(20, 12)[b % 2] for b in range(96)]),

@@ -20,7 +20,7 @@ def _lib():
 
 
 # B, T, Hq, Hkv, d, P, lens, n_nodes: pieces of one unit in many CTAs, whole
-# units, row tiles on a team of four, rows copied one by one
+# units, row tiles on a team of three, rows copied one by one
 CASES = [
     (2, 3, 8, 2, 128, 16, [9001, 4], None),
     (40, 5, 16, 4, 64, 16, [(97 * i) % 500 + 1 for i in range(40)], [i % 6 for i in range(40)]),
