@@ -8,8 +8,12 @@
 //   Small pools (16384 table entries, 32768 pages, 256 sequences at most)
 //   run as one kernel: every CTA makes the plan for itself in shared memory,
 //   a few us of three dependent reads, and does its part of the copies.
-//   (With the plan in a kernel of its own 4 beams took 20.6 us, most of it
-//   two launches and five cluster barriers.)
+//   (With the plan in a kernel of its own, most of it launches and cluster
+//   barriers: 4 beams 18.5 us for 8.3, 128 sequences 24.7 for 14.4, 250 in
+//   16000 pages 22.7 for 18.5.  At 32700 pages the two are equal, 22.6; beyond
+//   the limits one kernel loses: 500 sequences 30.8 for 25.7, 256 in 60000
+//   pages 30.8 for 24.7.  Compaction likewise: 18.2 for 8.3 and 36.7 for 22.6,
+//   then 293 for 271 in 60000 pages.)
 //   Larger ones run as two: one cluster of eight CTAs makes the plan, its
 //   steps separated by cluster barriers, so it needs neither a cleared
 //   workspace nor a grid-wide wait; the second kernel writes the new tables
