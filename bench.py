@@ -19,7 +19,7 @@ the 8 TB/s / 2.25 PFLOP/s denominators.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl reference]
                     [--config longctx|longctx_sparse|specexec70b|serving|llama3_8b|tiny]
-                    [--only] [--no-cpu-baseline] [--split-prefix | --iteration]
+                    [--only] [--no-cpu-baseline] [--split-prefix | --iteration | --paged]
 
 --iteration replays one whole speculative iteration (tree expansion with a
 random-weight drafter stand-in, a random-weight target layer and
@@ -28,6 +28,10 @@ tree_verify_attn, tree_accept, tree_commit_kv) from a single CUDA graph.
 --split-prefix times the long-context attention with each sequence's prefix
 split across the N ranks (prefix-only partials, NCCL all-gather, the
 log-sum-exp merge kernel): strong scaling of one layer's verification.
+
+--paged times the calls over a paged cache: the cases of perf/operators.py
+and further forms, each call after another over three sets of inputs in turn
+(the small cases' inputs stay in the L2).
 
 Timing: the step's calls are captured once into one CUDA graph (and each
 call into a graph of its own); W untimed warm-up steps, then K steps of the
@@ -1073,6 +1077,71 @@ def run_iteration(args, rank, world, dev, flush):
     del g
 
 
+def paged_cases():
+    """The cases of perf/operators.py, and forms of the same calls beside them."""
+    from perf import operators
+
+    def attn(name, **kw):
+        c = dict(name=name, op="attn", B=64, T=1, Hq=64, Hkv=8, d=128, P=16, lo=512, hi=8000, dtype="bf16", tree="bfs",
+                 ragged=False)
+        return dict(c, **kw)
+
+    pool = dict(B=256, layers=1, pages=60000, W=128, P=16, Hkv=8, d=128, dtype="bf16", lo=17, hi=1900)
+    accept = dict(op="accept", mode="specexec", tree="depth", ragged=True)
+    return operators, operators.listed() + [
+        attn("attn_tokens"), attn("attn_tokens_pages_of_5", P=5), attn("attn_tokens_pages_of_1", P=1),
+        attn("attn_short_tokens", B=256, lo=512, hi=512), attn("attn_short_trees", B=128, T=16, lo=512, hi=512),
+        attn("attn_one_long", B=1, T=16, lo=262144, hi=262144), attn("attn_three_row_tiles", B=16, T=40, lo=4000, hi=8000),
+        attn("attn_d64", T=4, d=64, P=32), attn("attn_d64_short_tokens", B=256, d=64, lo=400, hi=700),
+        attn("attn_fp32", B=16, T=8, Hq=32, lo=512, hi=4096, dtype="fp32"),
+        attn("attn_bf16_d32", B=16, T=8, Hq=32, d=32, lo=512, hi=4096),
+        attn("attn_bf16_3000_nodes", B=1, T=3000, Hq=8, Hkv=2, lo=512, hi=512, tree="depth"),
+        dict(accept, name="accept_specexec_chain", B=1, T=5, V=32000), dict(accept, name="accept_specexec_trees", B=32, T=16,
+                                                                          V=152064),
+        dict(pool, name="update_large_pool", op="update", fan=4, grow=16),
+        dict(pool, name="compact_large_pool", op="compact", pinned=False)]
+
+
+def run_paged(args, rank, world, dev, flush):
+    """Microseconds a call of the paged calls, one case after another: three sets of inputs in turn, warm-up, then
+    args.steps calls between two events on the launching stream; beside them the floor (bytes and operations that the
+    call cannot do without, at the measured peaks)."""
+    operators, cases = paged_cases()
+    hbm, bf16, _, src = peaks()
+    operators.own = True
+    out, total = {}, 0.0
+    clk = ClockSampler(torch.cuda.current_device())
+    clk.start()
+    for c in cases:
+        states = [operators.prepare(c, seed) for seed in range(3)]
+        for i in range(max(3, args.warmup)):
+            operators.run(states[i % 3])
+        torch.cuda.synchronize()
+        barrier(world)
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for i in range(args.steps):
+            operators.run(states[i % 3])
+        e1.record()
+        torch.cuda.synchronize()
+        us = max_over_ranks(e0.elapsed_time(e1) / args.steps, world) * 1e3
+        w = operators.work(c)
+        floor = max(w["bytes"] / (hbm * 1e9), w["flops"] / (bf16 * 1e12)) * 1e6
+        out[c["name"]] = {"us": round(us, 2), "floor_us": round(floor, 2), "gbs": round(w["bytes"] / us * 1e-3, 1),
+                          "tflops": round(w["flops"] / us * 1e-6, 1)}
+        total += us
+        del states
+        torch.cuda.empty_cache()
+    line = {"metric": "microseconds of one call of every paged case, summed", "value": total, "unit": "us", "n_gpus": world,
+            "steps": args.steps, "warmup": max(3, args.warmup), "ms_per_step": total * 1e-3, "higher_is_better": False,
+            "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic", "peaks": src,
+            "config": {"workload": "paged cases of perf/operators.py and further forms", "inputs": "three sets in turn",
+                       "parallelism": f"replicas x{world}"},
+            "cases": out, "clocks": clk.stop()}
+    if rank == 0:
+        print(json.dumps(line), flush=True)
+
+
 def main_roofline(step, ms, hbm, bf16, src):
     """The roofline object of the step's dominant call."""
     attn_s, acc_s = ms["attn"] * 1e-3, ms["accept"] * 1e-3
@@ -1144,6 +1213,7 @@ def main():
                     help="long-context attention with the prefix split across the ranks (strong scaling)")
     ap.add_argument("--iteration", action="store_true",
                     help="the whole speculative iteration (expand, verify, accept, commit) as one CUDA graph")
+    ap.add_argument("--paged", action="store_true", help="the calls over a paged cache, one case after another")
     args = ap.parse_args()
     if args.warmup < 3:
         args.warmup = 3
@@ -1157,8 +1227,9 @@ def main():
     build.build()
     dev = torch.device("cuda", torch.cuda.current_device())
     flush = torch.empty(256 << 20, dtype=torch.uint8, device=dev)
-    if args.split_prefix or args.iteration:
-        (run_split_prefix if args.split_prefix else run_iteration)(args, rank, world, dev, flush)
+    if args.split_prefix or args.iteration or args.paged:
+        mode = run_split_prefix if args.split_prefix else (run_iteration if args.iteration else run_paged)
+        mode(args, rank, world, dev, flush)
         if world > 1:
             import torch.distributed as dist
             dist.destroy_process_group()
