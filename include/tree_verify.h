@@ -480,7 +480,8 @@ TV_API int32_t tv_attn_paged_path(const tv_attn_paged_args* a);
  * read: a negative or non-finite probability, a row to sample from that has
  * no positive entry, or a uniform outside [0, 1) stops the walk with bonus
  * -1 (TV_DEV_NONFINITE).
- * 1 <= V <= 2^30, T <= 4096 (TV_ERR_UNSUPPORTED beyond).  No workspace.
+ * 1 <= V <= 2^30, T <= 4096, B <= 16384 (TV_ERR_UNSUPPORTED beyond); rows of
+ * one sequence do not overlap (tp_st, dp_st >= V where T > 1).  No workspace.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int32_t B, T, V;
@@ -511,7 +512,7 @@ TV_API tv_status tree_accept_probs(const tv_accept_probs_args* a, tv_stream_t st
  * Layouts: the pool as above with layer stride kv_sl; k_tree, v_tree
  * [layers][B][T][Hkv][d] (kt_sl, kt_sb, kt_st, kt_sh).  The tree K/V may not
  * overlap the pool, and no two sequences may commit into one page.
- * dtype TV_FP32 or TV_BF16, 1 <= d <= 1024, B <= 16384.
+ * dtype TV_FP32 or TV_BF16, 1 <= d <= 1024, B <= 16384, layers <= 65535.
  * Faults: n outside [0, T-1], L negative or L + n + 1 > max_pages *
  * page_size or > 2^31 - 1 -> TV_DEV_BAD_LEN; a path node outside [1, T) or
  * a path that does not increase -> TV_DEV_BAD_ROW; a page of the rows written outside
@@ -567,8 +568,8 @@ TV_API tv_status tree_commit_kv_paged(const tv_commit_paged_args* a, void* ws, s
  * Layouts: page_table [B_in][max_pages_in] (pt_sb), page_table_out
  * [B][max_pages] (po_sb), which may not overlap page_table; source, keep,
  * grow [B] int32; pinned [num_pages] int32 or NULL; n_free [1] or NULL.
- * Limits: dtype TV_FP32 or TV_BF16, d <= 1024, B <= 16384, num_pages <=
- * 2^24, B * max_pages < 2^31 (TV_ERR_UNSUPPORTED beyond).
+ * Limits: dtype TV_FP32 or TV_BF16, d <= 1024, B, B_in <= 16384, layers <=
+ * 65535, num_pages <= 2^24, B * max_pages < 2^31 (TV_ERR_UNSUPPORTED beyond).
  * Faults: source outside [-1, B_in) -> TV_DEV_BAD_ROW; keep or grow
  * negative, keep > max_pages_in * page_size or keep + grow > max_pages *
  * page_size -> TV_DEV_BAD_LEN; a kept page outside [0, num_pages) ->

@@ -27,11 +27,12 @@
 // it (a pass of 1200 elements a warp, loads and sums unrolled by 5 steps:
 // 6.6 us).
 // Bound by the chain of those latencies, not by bytes: one sequence of 5
-// nodes over V = 32000 takes 9.4 us; 8 sequences of up to 16 nodes over
-// V = 152064 17.5 us, 32 of them 34 us, since a CTA with its rows fills an SM
-// and 256 CTAs are two waves.  (Two CTAs an SM that hold p alone and read q
-// anew each pass: 30 us there, but 41 for 34 with 128 sequences over
-// V = 32000.)
+// nodes over V = 32000 takes 10 to 11 us; 8 sequences of up to 16 nodes over
+// V = 152064 17.5 us, 32 of them 38 to 40 (34 to 36 where the rows lie in the
+// L2), since a CTA with its rows fills an SM and 256 CTAs are two waves.
+// Deterministic trees, p alone: 8.6 and 21 us.  (Two CTAs an SM that hold p
+// alone and read q anew each pass: 30 us for 34 there, but 41 for 34 with 128
+// sequences over V = 32000, all with rows in the L2.)
 #include <cooperative_groups.h>
 
 #include <algorithm>

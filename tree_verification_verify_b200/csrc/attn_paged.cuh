@@ -289,7 +289,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Places of the line behind a unit's tiles, at most.  On the tensor cores a
 // border costs 5 us, 3 to 4 tiles' time: with none, CTAs of one piece were
 // done after 185 us and those of ten after 234 (32 sequences of 16 to 64
-// nodes, prefixes up to 16384); the call takes 245 us so and 220 with 3.
+// nodes, prefixes up to 16384); the call took 245 us so and 220 with 3.
 // CUDA cores: 255 us with 0, 248 with 1, 257 with 3 (16 sequences, fp32).
 constexpr int kPagedSimtCost = 1, kPagedTcCost = 3;
 

@@ -11,14 +11,16 @@
 //
 // What bounds it.  A steady tile takes about 2450 cycles (1.4 us) against 1024
 // each of the tensor pipe and the exponentials: with up to 128 rows a sequence
-// that is HBM (one sequence of 262144 rows, 16 nodes of 8 heads: 195 us, 5.5
-// TB/s; 32 sequences of up to 16 nodes on 512 to 16384 rows: 222 us, 5.2
-// TB/s), with more rows what the L2 hands the SMs, about 7 TB/s (two
-// sequences of 65537 to 131072 rows, 64 nodes of 4 heads: 245 us, 840
-// TFLOP/s; without the softmax's arithmetic, 207).  Beside the tiles: 5 to 8
-// us from the start to the first product, 5 us a border between units, 6 us
-// for the second kernel; those are most of a small call (one token on 700
-// rows: 16.4 us).
+// that is HBM (one sequence of 262144 rows, 16 nodes of 8 heads: 197 us, 5.4
+// TB/s; 32 sequences of up to 16 nodes on 512 to 16384 rows: 217 us, 5.3
+// TB/s; 64 single tokens on 512 to 8000 rows: 192 us, 5.8 TB/s), with more
+// rows what the L2 hands the SMs, about 7 TB/s (two sequences of 65537 to
+// 131072 rows, 64 nodes of 4 heads: 246 us, 838 TFLOP/s).  Those are short
+// runs at 1965 MHz; in long ones, under the power cap, the second takes 258 us
+// and the last 296.  Beside the tiles: 5 to 8 us from the start to the first
+// product, 5 us a border between units (256 single tokens on 512 rows: 162 us,
+// 85 for their bytes), 6 us for the second kernel; those are most of a small
+// call (one token on 700 rows: 16.4 us).
 //
 // Warp roles (384 threads):
 //   warps 0-7  softmax and output: two warpgroups, a thread per query row

@@ -18,11 +18,11 @@
 //   steps separated by cluster barriers, so it needs neither a cleared
 //   workspace nor a grid-wide wait; the second kernel writes the new tables
 //   and copies the rows over the whole GPU.
-// Measured: commit of 32 paths of up to 16 rows in 32 layers 10.7 us (38 MB);
-// update of 128 sequences in a pool of 1200 pages of 64 rows, 2 layers 16.6 us
-// (29 MB); compaction of 3500 pages of 16 rows, 2 layers 37 us (153 MB); 4
-// sequences 8.2 us each.  The plan's dependent reads bound the small ones,
-// HBM the copies.
+// Measured: commit of 32 paths of up to 16 rows in 32 layers 14.4 us (38 MB;
+// 10.3 where the rows lie in the L2); update of 128 sequences in a pool of 1200
+// pages of 64 rows, 2 layers 17.2 us (29 MB); compaction of 3500 pages of 16
+// rows, 2 layers 37 us (153 MB), of 60000 pages 271 us (1.5 GB); 4 sequences 8.4
+// us each.  The plan's dependent reads bound the small ones, HBM the copies.
 // Results depend on ranks alone, never on the order in which threads arrive.
 #include <cooperative_groups.h>
 
