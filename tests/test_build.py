@@ -11,9 +11,9 @@ from tree_verification_verify_b200 import build as b
 
 @pytest.fixture
 def tools(tmp_path, monkeypatch):
-    """Compilers that note their runs and write their output file."""
+    """Compilers that note their runs and write their arguments to their output file."""
     log = tmp_path / "log"
-    script = '#!/bin/sh\necho $0 >> %s\nwhile [ "$1" != -o ]; do shift; done\n%secho x > $2\n%s'
+    script = '#!/bin/sh\necho $0 >> %s\nall="$*"\nwhile [ "$1" != -o ]; do shift; done\n%secho "$all" > $2\n%s'
 
     def tool(name, before="", after=""):
         path = tmp_path / name
@@ -23,7 +23,6 @@ def tools(tmp_path, monkeypatch):
 
     monkeypatch.setattr(b, "LIB", str(tmp_path / "lib.so"))
     monkeypatch.setattr(b, "BINDING", str(tmp_path / "binding.so"))
-    monkeypatch.setattr(b, "BINDING_FOR", str(tmp_path / "_build" / "for.txt"))
     monkeypatch.setenv("NVCC", tool("nvcc"))
     monkeypatch.setenv("CXX", tool("cxx"))
 
@@ -54,6 +53,11 @@ def test_another_torch_rebuilds_the_binding(tools, monkeypatch):
     assert tools.runs() == ["cxx"]
     b.build()
     assert tools.runs() == []
+
+
+def test_the_binding_says_what_it_was_built_against():
+    b.build()
+    assert b.binding_built_against() == b.binding_against()
 
 
 def test_a_binding_of_another_torch_is_not_loaded(monkeypatch):

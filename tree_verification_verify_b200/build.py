@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -28,7 +29,6 @@ NVCC_FLAGS = [
 
 BINDING = os.path.join(HERE, "_paged.so")
 BINDING_SRC = os.path.join(CSRC, "paged_binding.cpp")
-BINDING_FOR = os.path.join(HERE, "_build", "paged_binding.txt")     # what the binding was built against
 
 
 def sources():
@@ -57,10 +57,12 @@ def binding_against() -> str:
 
 
 def binding_built_against() -> str:
-    if not os.path.exists(BINDING_FOR):
+    """What the binding says it was built against (its source has the text as a string); empty: nothing."""
+    if not os.path.exists(BINDING):
         return ""
-    with open(BINDING_FOR) as f:
-        return f.read()
+    with open(BINDING, "rb") as f:
+        found = re.search(rb"tv_paged built against ([^;]*);", f.read())
+    return found.group(1).decode() if found else ""
 
 
 def _binding_stale() -> bool:
@@ -75,7 +77,8 @@ def binding_command(out: str):
     inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [f"-I{i}" for i in inc] + \
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DTV_BUILT_AGAINST="tv_paged built against {binding_against()};"'] + [f"-I{i}" for i in inc] + \
         [BINDING_SRC, "-o", out, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
          "-lc10_cuda", "-L" + os.path.join(cuda, "lib64"), "-lcudart"]
 
@@ -108,18 +111,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     jobs = []
     if force or _stale():
         jobs.append((LIB, [nvcc] + NVCC_FLAGS + ["-I", os.path.join(ROOT, "include")] + sources() + ["-o", LIB + ".tmp"]))
-    binding = force or _binding_stale()
-    if binding:
+    if force or _binding_stale():
         jobs.append((BINDING, binding_command(BINDING + ".tmp")))
     errors = _run(jobs, verbose)
     if LIB in errors:
         raise errors[LIB]
     if BINDING in errors:
         warnings.warn(f"the binding of the paged calls was not built ({errors[BINDING]}); {LIB} was")
-    elif binding:
-        os.makedirs(os.path.dirname(BINDING_FOR), exist_ok=True)
-        with open(BINDING_FOR, "w") as f:
-            f.write(binding_against())
     return LIB
 
 

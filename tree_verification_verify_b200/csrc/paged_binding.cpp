@@ -17,6 +17,10 @@
 
 #include "../../include/tree_verify.h"
 
+// The torch and Python this is built for, for the build and the package to look
+// up without loading it.
+extern "C" __attribute__((used, visibility("default"))) const char tv_paged_built_against[] = TV_BUILT_AGAINST;
+
 namespace {
 
 // ------------------------------------------------------------------ errors

@@ -121,10 +121,10 @@ def binding():
             raise _tv.TVError(f"{BINDING_PATH} is missing: build it with "
                               "`python -m tree_verification_verify_b200.build`")
         from . import build
-        if build.binding_built_against() != build.binding_against():
-            raise _tv.TVError(f"{BINDING_PATH} was built against {build.binding_built_against() or 'an unknown torch'}, "
-                              f"this is {build.binding_against()}: build it again with "
-                              "`python -m tree_verification_verify_b200.build`")
+        built = build.binding_built_against()
+        if built not in ("", build.binding_against()):
+            raise _tv.TVError(f"{BINDING_PATH} was built against {built}, this is {build.binding_against()}: build it "
+                              "again with `python -m tree_verification_verify_b200.build`")
         from . import _paged
         L = _tv.lib()
         _paged.init({n: ctypes.cast(getattr(L, n), c_vp).value for n in _FUNCTIONS}, _tv.TVError)
